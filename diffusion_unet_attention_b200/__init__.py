@@ -15,6 +15,8 @@ Variants of the partially fused form: the page's reduction as a kernel of its
 own over a stored A (`qk_scores`, `row_stats`, then `softmax_av`), and A
 stored in fp16 (`qk_stats_f16a`, `softmax_av_f16a`).  Beside attention, the
 two specialised UNet kernels of the same section: `group_norm` and `geglu`.
+Around attention, the rest of the transformer block: `layer_norm` with its
+backward pass `layer_norm_backward`.
 
 This module only marshals torch tensors (device memory and streams) into the
 C ABI of libsdattn.so; all arithmetic runs in the CUDA kernels.  There is no
@@ -31,6 +33,7 @@ from . import _lib
 
 __all__ = ["qk_stats", "softmax_av", "flash", "flash_f32o", "flash_tf32", "partially_fused", "qk_scores", "row_stats", "qk_stats_f16a",
            "softmax_av_f16a", "group_norm", "geglu", "wino_filter", "conv3x3_winograd", "wino_workspace_bytes",
+           "layer_norm", "layer_norm_backward",
            "device_error", "a_ld", "a16_ld", "workspace_bytes", "SdattnError", "load_library"]
 
 SdattnError = _lib.SdattnError
@@ -417,6 +420,102 @@ def conv3x3_winograd(x: torch.Tensor, U: torch.Tensor, bias: torch.Tensor | None
 
 def wino_workspace_bytes(N: int, C: int, K: int, H: int, W: int, dtype=torch.float16) -> int:
     return int(_lib_handle().sdattn_wino_workspace_bytes(ctypes.byref(_conv_desc(N, C, K, H, W, dtype))))
+
+
+def _call(device: torch.device, fn: str, *args) -> None:
+    """Calls the library's `fn` with `device` current, the stream (the last
+    argument) being the device's current one; raises on a status."""
+    f = getattr(_lib_handle(), fn)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream(device))
+    _lib.check(fn, st)
+
+
+def _query(device: torch.device, fn: str, *args) -> int:
+    """The library's size query `fn`, asked with `device` current."""
+    with torch.cuda.device(device):
+        return int(getattr(_lib_handle(), fn)(*args))
+
+
+def _same_device(x: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must live on {x.device}")
+
+
+def _vector(t: torch.Tensor | None, n: int, device: torch.device, name: str) -> torch.Tensor | None:
+    """A parameter vector as contiguous fp32 [n] on `device`."""
+    if t is None:
+        return None
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}]")
+    return _contig(t.to(device=device, dtype=torch.float32))
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _out(out: torch.Tensor | None, shape, dtype: torch.dtype, device: torch.device, name: str = "out") -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
+    return out
+
+
+_LN_DTYPES = {**_DTYPES, torch.float32: _lib.SDATTN_F32}
+
+
+def _ln_desc(x: torch.Tensor, eps: float) -> _lib.LNDesc:
+    if not x.is_cuda or x.dim() < 1:
+        raise ValueError("x must be a CUDA tensor [..., C]")
+    if x.dtype not in _LN_DTYPES:
+        raise TypeError(f"dtype {x.dtype} not supported (float16, bfloat16 or float32)")
+    C = x.shape[-1]
+    if C < 1:
+        raise ValueError("rows must have at least one value")
+    return _lib.LNDesc(x.numel() // C, C, _LN_DTYPES[x.dtype], float(eps))
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-5, out: torch.Tensor | None = None, return_stats: bool = False):
+    """Layer normalisation over the last dimension of x [..., C] (fp16, bf16 or
+    fp32; C up to 8192), with fp32 gamma and beta [C] (None: ones, zeros).
+
+    With `return_stats` returns (y, stats), stats [..., 2] fp32 = (mean,
+    1 / sqrt(var + eps)) of every row, as `layer_norm_backward` takes it."""
+    desc = _ln_desc(x, eps)
+    g, b = _vector(gamma, desc.C, x.device, "gamma"), _vector(beta, desc.C, x.device, "beta")
+    x = _contig(x)
+    y = _out(out, x.shape, x.dtype, x.device)
+    stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device) if return_stats else None
+    _call(x.device, "sdattn_layer_norm", ctypes.byref(desc), x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
+    return (y, stats) if return_stats else y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamma: torch.Tensor | None = None):
+    """Gradients of `layer_norm`: (dx, dgamma, dbeta) from dy (x's shape and
+    dtype), the forward's x and stats, and gamma.  dx has x's dtype, dgamma and
+    dbeta are fp32 [C]; repeated calls give identical bits."""
+    desc = _ln_desc(x, 0.0)
+    _same_device(x, dy=dy, stats=stats)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must match x in shape and dtype")
+    if stats.shape != x.shape[:-1] + (2,) or stats.dtype != torch.float32:
+        raise ValueError("stats must be layer_norm's fp32 [..., 2]")
+    g = _vector(gamma, desc.C, x.device, "gamma")
+    dy, x, stats = _contig(dy), _contig(x), _contig(stats)
+    dx = torch.empty_like(x)
+    dgb = torch.empty((2, desc.C), dtype=torch.float32, device=x.device)
+    ws = torch.empty(_query(x.device, "sdattn_layer_norm_bwd_workspace_bytes", ctypes.byref(desc)), dtype=torch.uint8,
+                     device=x.device)
+    _call(x.device, "sdattn_layer_norm_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
+          dx.data_ptr(), dgb[0].data_ptr(), dgb[1].data_ptr(), ws.data_ptr(), ws.numel())
+    return dx, dgb[0], dgb[1]
 
 
 def device_error():

@@ -32,6 +32,7 @@ EXPORTS = ("sdattn_a_ld", "sdattn_workspace_bytes", "sdattn_qk_stats", "sdattn_s
            "sdattn_qk_scores", "sdattn_row_stats", "sdattn_a16_ld", "sdattn_qk_stats_f16a",
            "sdattn_softmax_av_f16a", "sdattn_group_norm", "sdattn_geglu", "sdattn_qk_stats_noalloc",
            "sdattn_wino_filter_bytes", "sdattn_wino_workspace_bytes", "sdattn_wino_filter", "sdattn_wino_conv3x3",
+           "sdattn_layer_norm", "sdattn_layer_norm_bwd_workspace_bytes", "sdattn_layer_norm_bwd",
            "sdattn_device_error", "sdattn_status_string", "sdattn_version")
 
 
@@ -51,6 +52,11 @@ class ConvDesc(ctypes.Structure):
     """sdattn_conv_desc: shape of one 3x3 convolution."""
     _fields_ = [("N", ctypes.c_int32), ("C", ctypes.c_int32), ("K", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("W", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LNDesc(ctypes.Structure):
+    """sdattn_ln_desc: shape of one layer normalisation."""
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class SdattnError(RuntimeError):
@@ -112,6 +118,13 @@ def load(path: str = LIB_PATH):
     lib.sdattn_wino_conv3x3.restype = ctypes.c_int
     lib.sdattn_qk_stats_noalloc.argtypes = [dp, vp, vp, vp, vp, vp]
     lib.sdattn_qk_stats_noalloc.restype = ctypes.c_int
+    np_ = ctypes.POINTER(LNDesc)
+    lib.sdattn_layer_norm.argtypes = [np_, vp, vp, vp, vp, vp, vp]
+    lib.sdattn_layer_norm.restype = ctypes.c_int
+    lib.sdattn_layer_norm_bwd_workspace_bytes.argtypes = [np_]
+    lib.sdattn_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.sdattn_layer_norm_bwd.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.sdattn_layer_norm_bwd.restype = ctypes.c_int
     lib.sdattn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.sdattn_device_error.restype = ctypes.c_int
     lib.sdattn_status_string.argtypes = [ctypes.c_int]

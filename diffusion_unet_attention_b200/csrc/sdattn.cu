@@ -9,13 +9,16 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "sdattn.h"
 
 #include "flash.cuh"
 #include "flash_tf32.cuh"
+#include "layer_norm.cuh"
 #include "qk_stats.cuh"
 #include "row_stats.cuh"
 #include "softmax_av.cuh"
@@ -789,6 +792,8 @@ sdattn_status dispatch_flash(const sdattn_desc* d, const void* Q, const void* K,
   return SDATTN_ERR_UNSUPPORTED;
 }
 
+#include "block_host.cuh"
+
 }  // namespace
 
 // ============================================================================
@@ -1079,6 +1084,72 @@ sdattn_status sdattn_wino_conv3x3(const sdattn_conv_desc* desc, const void* X, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return desc->dtype == SDATTN_BF16 ? launch_wino<true>(desc, X, U, bias, Y, ws, s)
                                     : launch_wino<false>(desc, X, U, bias, Y, ws, s);
+}
+
+// Partial rows of the backward pass's column sums.
+size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc) {
+  if (check_ln(desc) != SDATTN_OK) return 0;
+  // both access widths: the plan follows the pointers' alignment
+  const int dev = current_device();
+  const int nsm = sm_count(dev < 0 ? 0 : dev);
+  int64_t grid = 1;
+  for (bool vec : {false, true})
+    if (!vec || ln_vec(desc, {})) grid = std::max(grid, ln_bwd_grid(desc, plan_ln(desc, vec, true, nsm), nsm));
+  return static_cast<size_t>(grid) * 2 * desc->C * sizeof(float);
+}
+
+sdattn_status sdattn_layer_norm(const sdattn_ln_desc* desc, const void* X, const float* gamma, const float* beta,
+                                void* Y, float* stats, void* stream) {
+  const sdattn_status st = check_ln(desc);
+  if (st != SDATTN_OK) return st;
+  if (desc->T == 0) return SDATTN_OK;
+  if (!X || !Y) return SDATTN_ERR_INVALID_ARG;
+  const uintptr_t es = desc->dtype == SDATTN_F32 ? 4 : 2;
+  if (!aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(gamma, 4) || !aligned_to(beta, 4) || !aligned_to(stats, 8))
+    return SDATTN_ERR_ALIGNMENT;
+  const int dev = current_device();
+  if (dev < 0) return SDATTN_ERR_CUDA;
+  const LNPlan pl = plan_ln(desc, ln_vec(desc, {X, Y, gamma, beta}), false, sm_count(dev));
+  sdattn::LNParams p = {};
+  p.X = X;
+  p.Y = Y;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.stats = stats;
+  const int64_t rpc = pl.cta ? 1 : pl.threads / pl.L;
+  return launch_ln(desc, p, pl, false, (desc->T + rpc - 1) / rpc, static_cast<cudaStream_t>(stream));
+}
+
+sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, const void* X, const float* stats,
+                                    const float* gamma, void* dX, float* dgamma, float* dbeta, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const sdattn_status st = check_ln(desc);
+  if (st != SDATTN_OK) return st;
+  if (!dgamma || !dbeta || (desc->T > 0 && (!dY || !X || !stats || !dX))) return SDATTN_ERR_INVALID_ARG;
+  const uintptr_t es = desc->dtype == SDATTN_F32 ? 4 : 2;
+  if (!aligned_to(dY, es) || !aligned_to(X, es) || !aligned_to(dX, es) || !aligned_to(stats, 8) ||
+      !aligned_to(gamma, 4) || !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4))
+    return SDATTN_ERR_ALIGNMENT;
+  const int dev = current_device();
+  if (dev < 0) return SDATTN_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  const LNPlan pl = plan_ln(desc, ln_vec(desc, {dY, X, dX, gamma}), true, nsm);
+  const int64_t grid = ln_bwd_grid(desc, pl, nsm);   // 0 without rows: the sums are zero
+  if (!ws || ws_bytes < static_cast<size_t>(grid) * 2 * desc->C * sizeof(float)) return SDATTN_ERR_WORKSPACE;
+  if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  sdattn::LNParams p = {};
+  p.X = X;
+  p.dY = dY;
+  p.dX = dX;
+  p.gamma = gamma;
+  p.stats = const_cast<float*>(stats);
+  p.part = static_cast<float*>(ws);
+  if (grid > 0) {
+    const sdattn_status r = launch_ln(desc, p, pl, true, grid, s);
+    if (r != SDATTN_OK) return r;
+  }
+  return launch_column_sum(p.part, grid, 2 * desc->C, desc->C, dgamma, dbeta, s) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 const char* sdattn_status_string(sdattn_status status) {

@@ -79,7 +79,7 @@ extern "C" {
 typedef enum {
     SDATTN_F16 = 0,   /* IEEE binary16 */
     SDATTN_BF16 = 1,  /* bfloat16 */
-    SDATTN_F32 = 2    /* IEEE binary32: sdattn_flash_tf32 only */
+    SDATTN_F32 = 2    /* IEEE binary32: sdattn_flash_tf32 and the layer norm only */
 } sdattn_dtype;
 
 /* Shape of one attention call.  scale is applied to Q K^T (1/sqrt(d) in SD). */
@@ -314,6 +314,41 @@ sdattn_status sdattn_wino_filter(const sdattn_conv_desc *desc, const void *Wt, v
  * 4-byte aligned.  Y may not overlap X, U or ws. */
 sdattn_status sdattn_wino_conv3x3(const sdattn_conv_desc *desc, const void *X, const void *U, const float *bias,
                                   void *Y, void *ws, size_t ws_bytes, void *stream);
+
+/* Shape of one layer normalisation: T rows of C values, row-major and
+ * contiguous, element type dtype (F16, BF16 or F32). */
+typedef struct {
+    int64_t T;        /* rows, 0 .. 2^31 - 1 */
+    int32_t C;        /* values per row, 1 .. 8192 (SDATTN_ERR_UNSUPPORTED above) */
+    int32_t dtype;    /* sdattn_dtype of X, Y, dY and dX */
+    float eps;        /* finite, >= 0; added to the variance */
+} sdattn_ln_desc;
+
+/* Layer normalisation, one launch, x read once and y written once:
+ *   mean_t = sum_c X[t][c] / C,  r_t = 1 / sqrt(sum_c (X[t][c] - mean_t)^2 / C + eps),
+ *   Y[t][c] = (X[t][c] - mean_t) r_t gamma[c] + beta[c]      (fp32 arithmetic, one rounding).
+ * X: input; gamma, beta: float32 [C], either may be NULL (ones, zeros); Y:
+ * output; stats: NULL, or float32 [T][2] (8-byte aligned) that receives
+ * (mean_t, r_t) for the backward pass.  X, Y need the element's alignment
+ * only; rows that are multiples of 16 bytes on 16-byte aligned pointers run
+ * with 16-byte accesses, others element by element.  T = 0 does nothing. */
+sdattn_status sdattn_layer_norm(const sdattn_ln_desc* desc, const void* X, const float* gamma, const float* beta,
+                                void* Y, float* stats, void* stream);
+
+/* Bytes of workspace sdattn_layer_norm_bwd needs on the current device; 0 for an invalid desc. */
+size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc);
+
+/* Layer normalisation, backward pass, from the forward's inputs and stats
+ * (desc->eps is not read).  With z = (X - mean) r and e = dY gamma:
+ *   dX[t][c] = r_t (e[t][c] - mean_c(e) - z[t][c] mean_c(e z)),
+ *   dgamma[c] = sum_t dY[t][c] z[t][c],   dbeta[c] = sum_t dY[t][c].
+ * dY, X, stats, gamma (or NULL: ones): inputs; dX, dgamma, dbeta (float32
+ * [C]): outputs, all written (zero sums when T = 0).  The sums run in a fixed
+ * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-
+ * owned, overwritten, no state between calls.  Two launches. */
+sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, const void* X, const float* stats,
+                                    const float* gamma, void* dX, float* dgamma, float* dbeta, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 /* Reads and clears this device's error word (synchronises the device).
  * Returns SDATTN_OK, SDATTN_ERR_TIMEOUT, or SDATTN_ERR_CUDA if it cannot be

@@ -46,6 +46,25 @@ def group_norm(x, gamma, beta, groups: int, eps: float):
     return (xhat * np.asarray(gamma, np.float64).reshape(shape) + np.asarray(beta, np.float64).reshape(shape))
 
 
+def layer_norm(x, gamma, beta, eps: float):
+    """LayerNorm in fp64 over the last axis.  Returns y and stats [..., 2] = (mean, 1 / sqrt(var + eps))."""
+    x = np.asarray(x, dtype=np.float64)
+    mean = x.mean(axis=-1, keepdims=True)
+    rstd = 1.0 / np.sqrt(((x - mean) ** 2).mean(axis=-1, keepdims=True) + eps)
+    y = (x - mean) * rstd * np.asarray(gamma, np.float64) + np.asarray(beta, np.float64)
+    return y, np.concatenate([mean, rstd], axis=-1)
+
+
+def layer_norm_backward(dy, x, stats, gamma):
+    """Gradients (dx, dgamma, dbeta) of sum(dy * layer_norm(x)) in fp64, from x [T, C] and its stats."""
+    dy, x, stats = (np.asarray(a, np.float64) for a in (dy, x, stats))
+    mean, rstd = stats[:, :1], stats[:, 1:]
+    z = (x - mean) * rstd
+    e = dy * np.asarray(gamma, np.float64)
+    dx = rstd * (e - e.mean(axis=1, keepdims=True) - z * (e * z).mean(axis=1, keepdims=True))
+    return dx, (dy * z).sum(axis=0), dy.sum(axis=0)
+
+
 def gelu(x):
     """Exact GELU in fp64: x/2 (1 + erf(x / sqrt(2)))."""
     x = np.asarray(x, dtype=np.float64)

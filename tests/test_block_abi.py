@@ -1,0 +1,61 @@
+"""Argument checks of the transformer block's operators, decided on the host
+before anything is enqueued (the pointers below are never dereferenced), and
+what their Python entry points refuse without a GPU."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from diffusion_unet_attention_b200 import _lib, build
+    build.build()
+    return _lib.load()
+
+
+OK = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 1)
+OFF4 = ctypes.c_void_p((1 << 20) + 4)
+
+
+def ln(T=64, C=320, dtype=0, eps=1e-5):
+    from diffusion_unet_attention_b200 import _lib
+    return ctypes.byref(_lib.LNDesc(T, C, dtype, eps))
+
+
+@pytest.mark.parametrize("kw,status", [(dict(T=-1), 1), (dict(C=0), 1), (dict(eps=-1e-5), 1), (dict(eps=float("nan")), 1),
+                                       (dict(dtype=3), 2), (dict(C=8193), 2), (dict(T=1 << 31), 2)])
+def test_layer_norm_descriptor(lib, kw, status):
+    d = ln(**kw)
+    assert lib.sdattn_layer_norm(d, OK, OK, OK, OK, OK, None) == status
+    assert lib.sdattn_layer_norm_bwd(d, OK, OK, OK, OK, OK, OK, OK, OK, 1 << 30, None) == status
+    assert lib.sdattn_layer_norm_bwd_workspace_bytes(d) == 0
+
+
+def test_layer_norm_pointers(lib):
+    fwd, bwd = lib.sdattn_layer_norm, lib.sdattn_layer_norm_bwd
+    assert fwd(None, OK, OK, OK, OK, OK, None) == 1
+    assert fwd(ln(), None, OK, OK, OK, OK, None) == 1
+    assert fwd(ln(), OK, OK, OK, None, OK, None) == 1
+    assert fwd(ln(), ODD, OK, OK, OK, OK, None) == 3
+    assert fwd(ln(), OK, ODD, OK, OK, OK, None) == 3
+    assert fwd(ln(), OK, OK, OK, OK, OFF4, None) == 3
+    assert fwd(ln(T=0), None, None, None, None, None, None) == 0     # nothing to do
+    need = lib.sdattn_layer_norm_bwd_workspace_bytes(ln())
+    assert need >= 2 * 320 * 4
+    assert bwd(ln(), OK, OK, OK, None, OK, OK, OK, None, need, None) in (4, 5)      # 5: no device to plan for
+    assert bwd(ln(), None, OK, OK, OK, OK, OK, OK, OK, need, None) == 1
+    assert bwd(ln(), OK, OK, None, OK, OK, OK, OK, OK, need, None) == 1
+    assert bwd(ln(), OK, OK, OK, OK, OK, None, OK, OK, need, None) == 1
+    assert bwd(ln(dtype=2), OK, ctypes.c_void_p((1 << 20) + 2), OK, OK, OK, OK, OK, OK, need, None) == 3
+
+
+def test_python_refuses_cpu_tensors():
+    import diffusion_unet_attention_b200 as sd
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        sd.layer_norm(x)
+    with pytest.raises(ValueError):
+        sd.layer_norm_backward(x, x, torch.zeros(4, 2))

@@ -16,7 +16,8 @@ own over a stored A (`qk_scores`, `row_stats`, then `softmax_av`), and A
 stored in fp16 (`qk_stats_f16a`, `softmax_av_f16a`).  Beside attention, the
 two specialised UNet kernels of the same section: `group_norm` and `geglu`.
 Around attention, the rest of the transformer block: `layer_norm` with its
-backward pass `layer_norm_backward`.
+backward pass `layer_norm_backward`, and the gated feed-forward `gated_ff`
+(projections, activation and product in one kernel) with `gated_ff_backward`.
 
 This module only marshals torch tensors (device memory and streams) into the
 C ABI of libsdattn.so; all arithmetic runs in the CUDA kernels.  There is no
@@ -33,7 +34,7 @@ from . import _lib
 
 __all__ = ["qk_stats", "softmax_av", "flash", "flash_f32o", "flash_tf32", "partially_fused", "qk_scores", "row_stats", "qk_stats_f16a",
            "softmax_av_f16a", "group_norm", "geglu", "wino_filter", "conv3x3_winograd", "wino_workspace_bytes",
-           "layer_norm", "layer_norm_backward",
+           "layer_norm", "layer_norm_backward", "gated_ff", "gated_ff_backward",
            "device_error", "a_ld", "a16_ld", "workspace_bytes", "SdattnError", "load_library"]
 
 SdattnError = _lib.SdattnError
@@ -452,7 +453,8 @@ def _vector(t: torch.Tensor | None, n: int, device: torch.device, name: str) -> 
         return None
     if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
-    return _contig(t.to(device=device, dtype=torch.float32))
+    t = _contig(t.to(device=device, dtype=torch.float32))
+    return t if t.data_ptr() % 16 == 0 else t.clone()      # a slice of a larger vector
 
 
 def _ptr(t: torch.Tensor | None):
@@ -516,6 +518,54 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     _call(x.device, "sdattn_layer_norm_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
           dx.data_ptr(), dgb[0].data_ptr(), dgb[1].data_ptr(), ws.data_ptr(), ws.numel())
     return dx, dgb[0], dgb[1]
+
+
+def _ff_desc(x: torch.Tensor, w: torch.Tensor) -> _lib.FFDesc:
+    if not x.is_cuda or x.dim() < 1:
+        raise ValueError("x must be a CUDA tensor [..., C]")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"dtype {x.dtype} not supported (float16 or bfloat16)")
+    C = x.shape[-1]
+    if w.dim() != 2 or w.shape[1] != C or w.shape[0] % 2 or w.dtype != x.dtype:
+        raise ValueError(f"w must be [2F, {C}] of x's dtype")
+    _same_device(x, w=w)
+    if C < 1 or w.shape[0] < 2:
+        raise ValueError("widths must be at least 1")
+    return _lib.FFDesc(x.numel() // C, C, w.shape[0] // 2, _DTYPES[x.dtype])
+
+
+def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The UNet's gated feed-forward in one launch: with p = x w^T + bias,
+    p[..., :F] * GELU(p[..., F:]) (the activation of `geglu`), p never stored.
+
+    x [..., C] and w [2F, C] (fp16 or bf16), fp32 bias [2F] or None; returns
+    [..., F].  C and F must be multiples of 8."""
+    desc = _ff_desc(x, w)
+    b = _vector(bias, 2 * desc.F, x.device, "bias")
+    x, w = _contig(x), _contig(w)
+    y = _out(out, x.shape[:-1] + (desc.F,), x.dtype, x.device)
+    _call(x.device, "sdattn_gated_ff", ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
+    return y
+
+
+def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None):
+    """Gradients of `gated_ff`: (dx, dw, dbias) from dy [..., F] and the
+    forward's inputs (the projection is computed again).  dx and dw have x's
+    dtype; dbias is fp32 [2F], or None without a bias.  Repeated calls give
+    identical bits."""
+    desc = _ff_desc(x, w)
+    _same_device(x, dy=dy)
+    if dy.shape != x.shape[:-1] + (desc.F,) or dy.dtype != x.dtype:
+        raise ValueError(f"dy must be x.shape[:-1] + ({desc.F},) of x's dtype")
+    b = _vector(bias, 2 * desc.F, x.device, "bias")
+    dy, x, w = _contig(dy), _contig(x), _contig(w)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    db = torch.empty(2 * desc.F, dtype=torch.float32, device=x.device) if bias is not None else None
+    ws = torch.empty(_query(x.device, "sdattn_gated_ff_bwd_workspace_bytes", ctypes.byref(desc)), dtype=torch.uint8,
+                     device=x.device)
+    _call(x.device, "sdattn_gated_ff_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
+          dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), ws.numel())
+    return dx, dw, db
 
 
 def device_error():

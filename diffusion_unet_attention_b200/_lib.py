@@ -33,6 +33,7 @@ EXPORTS = ("sdattn_a_ld", "sdattn_workspace_bytes", "sdattn_qk_stats", "sdattn_s
            "sdattn_softmax_av_f16a", "sdattn_group_norm", "sdattn_geglu", "sdattn_qk_stats_noalloc",
            "sdattn_wino_filter_bytes", "sdattn_wino_workspace_bytes", "sdattn_wino_filter", "sdattn_wino_conv3x3",
            "sdattn_layer_norm", "sdattn_layer_norm_bwd_workspace_bytes", "sdattn_layer_norm_bwd",
+           "sdattn_gated_ff", "sdattn_gated_ff_bwd_workspace_bytes", "sdattn_gated_ff_bwd",
            "sdattn_device_error", "sdattn_status_string", "sdattn_version")
 
 
@@ -57,6 +58,11 @@ class ConvDesc(ctypes.Structure):
 class LNDesc(ctypes.Structure):
     """sdattn_ln_desc: shape of one layer normalisation."""
     _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class FFDesc(ctypes.Structure):
+    """sdattn_ff_desc: shape of one gated feed-forward."""
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class SdattnError(RuntimeError):
@@ -125,6 +131,13 @@ def load(path: str = LIB_PATH):
     lib.sdattn_layer_norm_bwd_workspace_bytes.restype = sz
     lib.sdattn_layer_norm_bwd.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdattn_layer_norm_bwd.restype = ctypes.c_int
+    fp = ctypes.POINTER(FFDesc)
+    lib.sdattn_gated_ff.argtypes = [fp, vp, vp, vp, vp, vp]
+    lib.sdattn_gated_ff.restype = ctypes.c_int
+    lib.sdattn_gated_ff_bwd_workspace_bytes.argtypes = [fp]
+    lib.sdattn_gated_ff_bwd_workspace_bytes.restype = sz
+    lib.sdattn_gated_ff_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.sdattn_gated_ff_bwd.restype = ctypes.c_int
     lib.sdattn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.sdattn_device_error.restype = ctypes.c_int
     lib.sdattn_status_string.argtypes = [ctypes.c_int]

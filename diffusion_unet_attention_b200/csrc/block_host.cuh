@@ -1,5 +1,5 @@
 // block_host.cuh -- argument checks, plans and launches of the transformer
-// block's operators around attention (layer norm).  Included by sdattn.cu
+// block's operators around attention (layer norm, gated feed-forward).  Included by sdattn.cu
 // after its launch helpers, inside its anonymous namespace.
 #pragma once
 
@@ -153,4 +153,182 @@ int64_t ln_bwd_grid(const sdattn_ln_desc* d, const LNPlan& pl, int nsm) {
 
 bool launch_column_sum(const float* part, int64_t P, int n, int n0, float* out0, float* out1, cudaStream_t s) {
   return launch(sdattn::column_sum_kernel, (n + 31) / 32, 1024, 0, s, part, P, n, n0, out0, out1);
+}
+
+// --------------------------------------------------------------------------
+// Gated feed-forward (gated_ff.cuh)
+// --------------------------------------------------------------------------
+sdattn_status check_ff(const sdattn_ff_desc* d) {
+  if (!d) return SDATTN_ERR_INVALID_ARG;
+  if (d->T < 0 || d->C < 1 || d->F < 1) return SDATTN_ERR_INVALID_ARG;
+  if (d->dtype != SDATTN_F16 && d->dtype != SDATTN_BF16) return SDATTN_ERR_UNSUPPORTED;
+  // rows of x, W and y are whole 16-byte units, as TMA needs; the bounds keep
+  // every tile count in 32 bits
+  if (d->C % 8 != 0 || d->F % 8 != 0 || d->C > 65536 || d->F > 65536 || d->T >= (int64_t(1) << 27))
+    return SDATTN_ERR_UNSUPPORTED;
+  return SDATTN_OK;
+}
+
+CUtensorMapDataType elem16(int dtype) {
+  return dtype == SDATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// Columns of h per tile (a multiple of 16 up to 128): the fewest waves of the
+// longest of a tile's products (2 clocks per column pair and 64 of C), loads
+// (64 bytes per clock and SM) and epilogue, plus one tile's epilogue at the
+// end.  Many rows give whole 128-column tiles; few rows narrower ones, until
+// there is about one tile per SM.
+int plan_gated(const sdattn_ff_desc* d, int nsm) {
+  const int64_t rts = (d->T + 127) / 128;
+  const double ksteps = (d->C + 63) / 64;
+  int best_hn = 128;
+  double best = 1e300;
+  for (int hn = 128; hn >= 16; hn -= 16) {
+    const int64_t tiles = rts * ((d->F + hn - 1) / hn);
+    const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
+    const double tile = std::max(ksteps * std::max(4.0 * hn, (16384.0 + 256.0 * hn) / 64.0), 24.0 * hn);
+    const double cost = waves * tile + 24.0 * hn;
+    if (cost < best) {
+      best = cost;
+      best_hn = hn;
+    }
+  }
+  return best_hn;
+}
+
+template <bool BF16, bool BWD>
+sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W, const float* bias, const void* dY,
+                           void* Y, float* part, cudaStream_t s) {
+  const int dev = current_device();
+  if (dev < 0) return SDATTN_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  const uint64_t T = d->T, C = d->C, F = d->F;
+  sdattn::GatedParams p;
+  p.bias = bias;
+  p.dY = dY;
+  p.Y = Y;
+  p.part = part;
+  p.T = static_cast<int>(T);
+  p.F = d->F;
+  p.hn = plan_gated(d, nsm);
+  p.rts = static_cast<int>((T + 127) / 128);
+  p.fts = (d->F + p.hn - 1) / p.hn;
+  p.ksteps = (d->C + 63) / 64;
+  const CUtensorMapDataType dt = elem16(d->dtype);
+  CUtensorMap mx, mw, my;
+  if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 128)) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mw, W, dt, C, F, 2, C * 2, F * C * 2, 64, static_cast<uint32_t>(p.hn))) return SDATTN_ERR_CUDA;
+  const uint64_t ldy = BWD ? 4 * F : 2 * F;   // bytes of a row of y, or of P = [dh, dg]
+  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, 64, 32)) return SDATTN_ERR_CUDA;
+  const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.fts));
+  constexpr int smem = sdattn::GatedSmem<BWD>::BYTES;
+  auto run = [&](auto kern, std::atomic<uint64_t>& done) {
+    if (!ensure_smem(kern, smem, done, dev)) return SDATTN_ERR_CUDA;
+    return launch(kern, grid, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+  };
+  static std::atomic<uint64_t> done_full{0}, done_part{0};
+  return p.hn == 128 ? run(sdattn::gated_kernel<BF16, BWD, true>, done_full)
+                     : run(sdattn::gated_kernel<BF16, BWD, false>, done_part);
+}
+
+// dx = P W and dW = P^T x: tiles, splits and where their partials lie.
+struct FFBwdPlan {
+  sdattn::ProductParams pp;
+  size_t p_bytes, db_bytes, part_bytes[2];
+  size_t total;
+};
+
+// A result's columns are cut into the fewest tiles of at most 256, rounded up
+// to whole slabs of 64.  With L the contraction steps an SM would run if both
+// products were shared out evenly, a contraction longer than 3/4 L is split
+// into pieces of about L / 2 (at least 8 steps: a piece costs a partial
+// result that is written and read again).
+FFBwdPlan plan_ff_bwd(const sdattn_ff_desc* d, int nsm) {
+  FFBwdPlan pl;
+  const int M[2] = {static_cast<int>(d->T), 2 * d->F}, K[2] = {2 * d->F, static_cast<int>(d->T)};
+  double total = 0;
+  for (int i = 0; i < 2; ++i) {
+    sdattn::ProductSide& s = pl.pp.s[i];
+    s.M = M[i];
+    s.N = d->C;
+    const int n = (s.N + 255) / 256;
+    s.bn = ((s.N + n - 1) / n + 63) / 64 * 64;
+    s.nts = (s.N + s.bn - 1) / s.bn;
+    s.mn = (s.M + 127) / 128 * s.nts;
+    s.ksteps = (K[i] + 63) / 64;
+    total += static_cast<double>(s.mn) * s.ksteps;
+  }
+  const double L = total / nsm;
+  size_t at = 0;
+  auto place = [&](size_t bytes) { at += (bytes + 255) / 256 * 256; return bytes; };
+  pl.p_bytes = place(static_cast<size_t>(d->T) * 2 * d->F * 2);
+  pl.db_bytes = place(static_cast<size_t>((d->T + 127) / 128) * 4 * 2 * d->F * 4);
+  for (int i = 0; i < 2; ++i) {
+    sdattn::ProductSide& s = pl.pp.s[i];
+    s.splits = 1;
+    if (s.ksteps > 0.75 * L)
+      s.splits = std::max(1, std::min(s.ksteps / 8, static_cast<int>(std::ceil(s.ksteps / (0.5 * L)))));
+    s.kper = (s.ksteps + s.splits - 1) / s.splits;
+    s.splits = (s.ksteps + s.kper - 1) / s.kper;
+    s.units = s.mn * s.splits;
+    pl.part_bytes[i] = s.splits > 1 ? place(static_cast<size_t>(s.splits) * s.M * s.N * 4) : 0;
+  }
+  pl.pp.first = pl.pp.s[1].kper >= pl.pp.s[0].kper ? 1 : 0;
+  pl.total = at;
+  return pl;
+}
+
+template <bool BF16>
+sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const void* dY, const void* X, const void* W,
+                            const float* bias, void* dX, void* dW, float* dbias, void* ws, cudaStream_t s) {
+  const int dev = current_device();
+  if (dev < 0) return SDATTN_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  auto take = [&](size_t bytes) {
+    uint8_t* r = at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  void* P = take(pl.p_bytes);
+  float* db_part = reinterpret_cast<float*>(take(pl.db_bytes));
+  float* parts[2] = {nullptr, nullptr};
+  for (int i = 0; i < 2; ++i)
+    if (pl.part_bytes[i] > 0) parts[i] = reinterpret_cast<float*>(take(pl.part_bytes[i]));
+
+  sdattn_status st = launch_gated<BF16, true>(d, X, W, bias, dY, P, dbias ? db_part : nullptr, s);
+  if (st != SDATTN_OK) return st;
+
+  const uint64_t T = d->T, C = d->C, F2 = 2 * uint64_t(d->F);
+  const CUtensorMapDataType dt = elem16(d->dtype);
+  CUtensorMap mpk, mpm, mw, mx, mo[2];
+  if (!make_map_3d(&mpk, P, dt, F2, T, 1, F2 * 2, T * F2 * 2, 64, 128)) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mpm, P, dt, F2, T, 1, F2 * 2, T * F2 * 2, 64, 64)) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mw, W, dt, C, F2, 1, C * 2, F2 * C * 2, 64, 64)) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 64)) return SDATTN_ERR_CUDA;
+  void* outs[2] = {dX, dW};
+  for (int i = 0; i < 2; ++i) {
+    const sdattn::ProductSide& sd = pl.pp.s[i];
+    const uint64_t M = sd.M;
+    const bool ok = sd.splits > 1
+                        ? make_map_3d(&mo[i], parts[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, C, M, sd.splits, C * 4, M * C * 4, 32, 32)
+                        : make_map_3d(&mo[i], outs[i], dt, C, M, 1, C * 2, M * C * 2, 64, 32);
+    if (!ok) return SDATTN_ERR_CUDA;
+  }
+  auto kern = sdattn::product_kernel<BF16>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kern, sdattn::ProductCfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
+  const int grid = std::min(nsm, pl.pp.s[0].units + pl.pp.s[1].units);
+  if (!launch(kern, grid, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
+    return SDATTN_ERR_CUDA;
+  for (int i = 0; i < 2; ++i) {
+    const sdattn::ProductSide& sd = pl.pp.s[i];
+    if (sd.splits == 1) continue;
+    const int64_t n = static_cast<int64_t>(sd.M) * sd.N;
+    const int g = static_cast<int>(std::min<int64_t>((n / 8 + 255) / 256, int64_t(nsm) * 8));
+    if (!launch(sdattn::add_splits_kernel<BF16>, g, 256, 0, s, parts[i], sd.splits, n, outs[i])) return SDATTN_ERR_CUDA;
+  }
+  if (dbias && !launch_column_sum(db_part, (d->T + 127) / 128 * 4, 2 * d->F, 2 * d->F, dbias, dbias, s))
+    return SDATTN_ERR_CUDA;
+  return SDATTN_OK;
 }

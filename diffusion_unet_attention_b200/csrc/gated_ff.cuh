@@ -1,0 +1,597 @@
+// gated_ff.cuh -- the gated feed-forward of the UNet's transformer block, both
+// projections, the activation and the product in one kernel, and its backward
+// pass.
+//
+//   h = x Wh^T + bh,  g = x Wg^T + bg        W [2F][C]: Wh its first F rows, Wg its last
+//   y = h GELU(g)                            GELU(g) = g Phi(g), exact (erf) form
+//
+//   backward, from x, W, b and dy alone (h and g are computed again: for the
+//   UNet's widths the product is cheaper than writing and reading them back):
+//   dh = dy GELU(g),  dg = dy h (Phi(g) + g phi(g)),   P = [dh, dg]   [T][2F]
+//   dx = P W,  dW = P^T x,  db = column sums of P
+//
+// gated_kernel     x, W (, dy) -> y, or P in 16 bits and partial sums of db
+// product_kernel   P, W, x -> dx and dW, one launch for both products
+// add_splits_kernel  partial products of a split contraction -> dx, dW
+//
+// All products run on the tensor cores (fp32 accumulators in tensor memory);
+// bias, activation and gradients are fp32.  Roundings to 16 bits: y, dx, dW
+// once; P once, because it is the tensor cores' operand in the two products
+// that follow (a relative 2^-9 / 2^-12 on average per entry, random, which the
+// products average out to about that of their own output rounding).  db is
+// summed from the unrounded fp32 entries of P.
+//
+// The pair of columns (h_f, g_f) must meet in one thread: a tile is 128 rows
+// by HN columns of h and the matching HN columns of g, both in one B operand
+// of 2 HN rows (two TMA boxes one under the other), so one tcgen05.mma of
+// N = 2 HN per 16 columns of C computes both and the epilogue finds h_f and
+// g_f in the same tensor-memory lane, HN columns apart.
+#pragma once
+
+#include "unet_ops.cuh"
+
+namespace sdattn {
+
+// Phi(g) and exp(-g^2 / 2) by the same approximation as gelu_erf.
+__device__ __forceinline__ void normal_cdf(float g, float& cdf, float& bell) {
+  constexpr float kP = 0.3275911f, kA1 = 0.254829592f, kA2 = -0.284496736f, kA3 = 1.421413741f,
+                  kA4 = -1.453152027f, kA5 = 1.061405429f;
+  constexpr float kRsqrt2 = 0.7071067811865476f, kL2E = 1.4426950408889634f;
+  const float x = fabsf(g) * kRsqrt2;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(kP, x, 1.f)));
+  bell = ex2_approx(-x * x * kL2E);
+  const float half_erfc = 0.5f * t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, kA5, kA4), kA3), kA2), kA1) * bell;
+  cdf = g >= 0.f ? 1.f - half_erfc : half_erfc;
+}
+
+// Sums v[i] over the warp's lanes for N columns at once (N a power of two up
+// to 32): each exchange halves the columns a lane still holds.  Lane l ends
+// with the total of column l / (32 / N); the order is fixed.
+template <int N>
+__device__ __forceinline__ float warp_column_sums(float* v, int lane) {
+  int s = 16;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1, s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[i + n / 2] : v[i], send = up ? v[i] : v[i + n / 2];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+    }
+  }
+  float t = v[0];
+  for (; s >= 1; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+  return t;
+}
+
+struct GatedCfg {
+  static constexpr int BK = 64;                     // columns of C per stage
+  static constexpr int A_BYTES = 128 * 128;         // 128 rows of x
+  static constexpr int HN = 128;                    // most columns of h (and of g) per tile
+  static constexpr int STAGE = A_BYTES + 2 * HN * 128;
+  static constexpr int NTHREADS = 384;              // TMA, MMA, two idle warps, eight epilogue warps
+  static constexpr uint32_t TMEM_COLS = 512;        // two accumulators of 2 HN columns
+};
+
+template <bool BWD>
+struct GatedSmem {
+  static constexpr int STAGES = BWD ? 3 : 4;
+  static constexpr int WSTG = BWD ? 8192 : 4096;    // an epilogue warp's staged output: 32 rows x 64 columns of y, or of dh and of dg
+  static constexpr int OFF_STG = STAGES * GatedCfg::STAGE;
+  static constexpr int OFF_BAR = OFF_STG + 8 * WSTG;
+  static constexpr int NBAR = 2 * STAGES + 4 + 1;
+  static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;
+  static_assert(BYTES <= 232448, "shared memory budget");
+};
+
+struct GatedParams {
+  const float* bias;    // [2F], on 16 bytes, or null
+  const void* dY;       // [T][F]      (backward)
+  void* Y;              // [T][F]; backward: P [T][2F]
+  float* part;          // [4 row tiles][2F] partial sums of db, or null
+  int T, F;
+  int hn;               // columns of h per tile: a multiple of 16, at most 128
+  int rts, fts;         // row tiles, column tiles
+  int ksteps;           // ceil(C / 64)
+};
+
+// y (or dh and dg) of 8 columns of one row, from the accumulators; bh: the h
+// columns' biases in global memory, g's F further (the same address in every
+// lane, so a broadcast out of L1), or null.
+template <bool BWD, bool BF16>
+__device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t* g, const float* bh, int F,
+                                               const uint4& dy, float* o0, float* o1) {
+  float b[16], d[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int src = 4 * (q & 1) + (q < 2 ? 0 : F);   // of h, then of g
+    const float4 v = bh != nullptr ? __ldg(reinterpret_cast<const float4*>(bh + src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    b[4 * q] = v.x;
+    b[4 * q + 1] = v.y;
+    b[4 * q + 2] = v.z;
+    b[4 * q + 3] = v.w;
+  }
+  if constexpr (BWD) unpack8<BF16>(dy, d);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float hv = __uint_as_float(h[e]) + b[e], gv = __uint_as_float(g[e]) + b[8 + e];
+    if constexpr (BWD) {
+      float cdf, bell;
+      normal_cdf(gv, cdf, bell);
+      o0[e] = d[e] * (gv * cdf);
+      o1[e] = d[e] * (hv * fmaf(gv * 0.3989422804014327f, bell, cdf));
+    } else {
+      o0[e] = hv * gelu_erf(gv);
+    }
+  }
+}
+
+// Roles: warp 0 TMA (a ring of x / W stages), warp 1 MMA (tcgen05 SS,
+// 128 x 2 hn x 16, two accumulators so that a tile's epilogue overlaps the
+// next tile's products), warps 4..11 epilogue: two warps per quarter of the
+// tile's rows, each taking half of its columns.  Whole tiles (hn = 128) leave
+// through shared memory and TMA stores of 32 rows x 64 columns, which also
+// clip at the edges; narrower ones are stored 16 bytes per thread.
+template <bool BF16, bool BWD, bool FULL>
+__global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
+    gated_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmY, const GatedParams p) {
+  using C = GatedCfg;
+  using S = GatedSmem<BWD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+  uint64_t* full = bars;                     // [STAGES] TMA -> MMA
+  uint64_t* empty = full + S::STAGES;        // [STAGES] MMA -> TMA
+  uint64_t* acc_full = empty + S::STAGES;    // [2] MMA -> epilogue
+  uint64_t* acc_empty = acc_full + 2;        // [2] epilogue -> MMA
+  uint64_t* drain_bar = acc_empty + 2;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);   // [0] tensor memory, [1] abort
+  volatile uint32_t* abort_flag = misc + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hn = FULL ? 128 : p.hn;
+  const int tiles = p.rts * p.fts;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    mbar_init(drain_bar, 1);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    if (FULL) tma_prefetch_desc(&tmY);
+  }
+  if (warp == 1) {
+    tmem_alloc(&misc[0], C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      const uint32_t bytes = C::A_BYTES + 2 * hn * 128;
+      uint32_t c = 0;
+      bool live = true;
+      for (int u = blockIdx.x; u < tiles && live; u += gridDim.x) {
+        const int rt = u / p.fts, ft = u - rt * p.fts;
+        for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
+          const uint32_t st = c % S::STAGES, n = c / S::STAGES;
+          if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
+          uint8_t* s = smem + st * C::STAGE;
+          mbar_arrive_expect_tx(&full[st], bytes);
+          tma_load_3d(s, &tmX, ks * C::BK, rt * 128, 0, &full[st]);
+          tma_load_3d(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, &full[st]);
+          tma_load_3d(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, &full[st]);
+        }
+      }
+      // every load this thread issued lands before the CTA can exit
+      volatile uint32_t never = 0;
+      for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
+        const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
+        mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer --------------------------------
+    const uint32_t idesc = idesc_f16(128, 2 * hn, BF16, false, false);
+    const uint32_t base = smem_u32(smem);
+    uint32_t c = 0, ui = 0;
+    bool live = true;
+    for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
+      tc_fence_after();
+      for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
+        const uint32_t st = c % S::STAGES, n = c / S::STAGES;
+        if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
+        tc_fence_after();
+        const uint32_t s = base + st * C::STAGE;
+#pragma unroll
+        for (int kk = 0; kk < C::BK / 16; ++kk)
+          mma_ss(tmem + ab * 256, sdesc_sw128(s + kk * 32, 16, 1024), sdesc_sw128(s + C::A_BYTES + kk * 32, 16, 1024),
+                 idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[st]);
+      }
+      if (live) mma_commit(&acc_full[ab]);
+    }
+    volatile uint32_t never = 0;
+    mma_commit(drain_bar);
+    mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+  } else if (warp >= 4) {
+    // ------------------------------ epilogue ----------------------------------
+    constexpr int CW = FULL ? 32 : 8;             // columns per pass
+    const int quarter = warp & 3, half = (warp - 4) >> 2, ew = warp - 4;
+    const int hw = hn / 2;                        // columns per warp
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* stg = smem + S::OFF_STG + ew * S::WSTG;
+    uint32_t ui = 0;
+    bool live = true;
+    for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
+      const int rt = u / p.fts, ft = u - rt * p.fts;
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      const int f0 = ft * hn + half * hw;         // this warp's first column of h
+      const int r0 = rt * 128 + quarter * 32, row = r0 + lane;
+      const bool row_ok = row < p.T;
+      live = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], na & 1, kSiteAccFull, abort_flag));
+      if (!live) break;
+      tc_fence_after();
+      if constexpr (FULL) {
+        if (lane == 0) bulk_wait_read<0>();   // the staging buffers' previous stores have read them
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < hw; c0 += CW) {
+        const int f = f0 + c0;
+        uint4 dy[CW / 8];
+        if constexpr (BWD) {
+          const uint16_t* src = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + f;
+#pragma unroll
+          for (int q = 0; q < CW / 8; ++q)
+            dy[q] = row_ok && f + 8 * q < p.F ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t h[CW], g[CW];
+        const uint32_t at = tmem + ab * 256 + half * hw + c0 + lane_off;
+        if constexpr (FULL) {
+          tmem_ld_x32(at, h);
+          tmem_ld_x32(at + hn, g);
+        } else {
+          tmem_ld_x8(at, h);
+          tmem_ld_x8(at + hn, g);
+        }
+        tmem_wait_ld();
+        reg_fence<CW>(h);
+        reg_fence<CW>(g);
+        float o0[CW], o1[CW];
+#pragma unroll
+        for (int q = 0; q < CW / 8; ++q) {
+          // columns past F (their accumulators are zero) take no bias
+          const float* bh = p.bias != nullptr && f + 8 * q < p.F ? p.bias + f + 8 * q : nullptr;
+          gated_columns8<BWD, BF16>(h + 8 * q, g + 8 * q, bh, p.F, dy[q], o0 + 8 * q, o1 + 8 * q);
+        }
+        if constexpr (FULL) {
+#pragma unroll
+          for (int q = 0; q < CW / 8; ++q) {
+            const int ch = ((c0 / 8 + q) ^ (lane & 7)) << 4;
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ch) = pack8<BF16>(o0 + 8 * q);
+            if constexpr (BWD) *reinterpret_cast<uint4*>(stg + 4096 + lane * 128 + ch) = pack8<BF16>(o1 + 8 * q);
+          }
+        } else if (row_ok && f < p.F) {
+          uint16_t* dst = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * (BWD ? 2 * p.F : p.F) + f;
+          *reinterpret_cast<uint4*>(dst) = pack8<BF16>(o0);
+          if constexpr (BWD) *reinterpret_cast<uint4*>(dst + p.F) = pack8<BF16>(o1);
+        }
+        if constexpr (BWD) {
+          if (p.part != nullptr) {
+            // rows past T add nothing, whatever their biases are
+#pragma unroll
+            for (int j = 0; j < CW; ++j) {
+              o0[j] = row_ok ? o0[j] : 0.f;
+              o1[j] = row_ok ? o1[j] : 0.f;
+            }
+            const float s0 = warp_column_sums<CW>(o0, lane), s1 = warp_column_sums<CW>(o1, lane);
+            const int j = lane / (32 / CW);
+            if (lane % (32 / CW) == 0 && f + j < p.F) {
+              float* dst = p.part + static_cast<int64_t>(rt * 4 + quarter) * 2 * p.F + f + j;
+              dst[0] = s0;
+              dst[p.F] = s1;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if constexpr (FULL) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&acc_empty[ab]);
+        if constexpr (FULL) {
+          // stores start inside the tensor; what runs over its edges is clipped
+          if (f0 < p.F && r0 < p.T) {
+            tma_store_3d(&tmY, stg, f0, r0, 0);
+            if constexpr (BWD) tma_store_3d(&tmY, stg + 4096, f0, r0, 1);
+            bulk_commit();
+          }
+        }
+      }
+    }
+    if (FULL && lane == 0) bulk_wait<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dx = P W and dW = P^T x in one launch.  A unit is a 128-row tile of one of
+// the two results, up to 256 of its columns, over one split of the
+// contraction; units of both results are dealt out in turn, so that neither
+// product leaves SMs idle while the other runs.
+//   dx: A = P [T][2F], K-major;  B = W [2F][C], N-major (its rows run along N)
+//   dW: A = P, M-major (P^T);    B = x [T][C], N-major
+// M- and N-major tiles are slabs of 64 columns x 64 contraction rows, 128-byte
+// swizzled.  A result whose contraction is split goes to fp32 partials that
+// add_splits_kernel adds in split order.
+// ---------------------------------------------------------------------------
+struct ProductCfg {
+  static constexpr int BK = 64;
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int SLAB = 64 * 128;             // 64 columns x 64 contraction rows
+  static constexpr int BN = 256;                    // most columns of a tile
+  static constexpr int STAGE = A_BYTES + BN / 64 * SLAB;
+  static constexpr int STAGES = 4;
+  static constexpr int OFF_STG = STAGES * STAGE;    // [8 warps] 32 rows x 128 bytes
+  static constexpr int OFF_BAR = OFF_STG + 8 * 4096;
+  static constexpr int NBAR = 2 * STAGES + 4 + 1;
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+  static constexpr int NTHREADS = 384;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct ProductSide {
+  int M, N;           // the result's rows and columns
+  int bn;             // columns per tile, a multiple of 64 up to 256
+  int nts;            // column tiles
+  int mn;             // row tiles x column tiles
+  int splits;         // of the contraction
+  int ksteps, kper;   // contraction steps of 64: in all, per split
+  int units;          // mn * splits
+};
+
+struct ProductParams {
+  ProductSide s[2];   // 0: dx, 1: dW
+  int first;          // the side whose units are longer: dealt out before the other's
+};
+
+struct ProductUnit {
+  int side, m0, n0, cols, split, k0, k1;
+};
+
+__device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, int u) {
+  ProductUnit r;
+  const int n1 = p.s[p.first].units;
+  r.side = u < n1 ? p.first : 1 - p.first;
+  if (u >= n1) u -= n1;
+  const ProductSide& s = p.s[r.side];
+  r.split = u / s.mn;
+  const int t = u - r.split * s.mn, mt = t / s.nts, nt = t - mt * s.nts;
+  r.m0 = mt * 128;
+  r.n0 = nt * s.bn;
+  r.cols = min(s.bn, s.N - r.n0);
+  r.k0 = r.split * s.kper;
+  r.k1 = min(s.ksteps, r.k0 + s.kper);
+  return r;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tmPk, const __grid_constant__ CUtensorMap tmPm,
+                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
+                   const __grid_constant__ ProductParams p) {
+  using C = ProductCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full = bars;
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain_bar = acc_empty + 2;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile uint32_t* abort_flag = misc + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.s[0].units + p.s[1].units;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    mbar_init(drain_bar, 1);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmPk);
+    tma_prefetch_desc(&tmPm);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmO0);
+    tma_prefetch_desc(&tmO1);
+  }
+  if (warp == 1) {
+    tmem_alloc(&misc[0], C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t c = 0;
+      bool live = true;
+      for (int u = blockIdx.x; u < units && live; u += gridDim.x) {
+        const ProductUnit t = product_unit(p, u);
+        const int slabs = (t.cols + 63) / 64;
+        const CUtensorMap* tmB = t.side == 0 ? &tmW : &tmX;
+        for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
+          const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+          if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
+          uint8_t* s = smem + st * C::STAGE;
+          mbar_arrive_expect_tx(&full[st], C::A_BYTES + slabs * C::SLAB);
+          if (t.side == 0) {
+            tma_load_3d(s, &tmPk, ks * C::BK, t.m0, 0, &full[st]);
+          } else {
+            tma_load_3d(s, &tmPm, t.m0, ks * C::BK, 0, &full[st]);
+            tma_load_3d(s + C::SLAB, &tmPm, t.m0 + 64, ks * C::BK, 0, &full[st]);
+          }
+          for (int j = 0; j < slabs; ++j)
+            tma_load_3d(s + C::A_BYTES + j * C::SLAB, tmB, t.n0 + 64 * j, ks * C::BK, 0, &full[st]);
+        }
+      }
+      volatile uint32_t never = 0;
+      for (uint32_t st = 0; st < C::STAGES && st < c; ++st) {
+        const uint32_t uses = (c - st + C::STAGES - 1) / C::STAGES;
+        mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t base = smem_u32(smem);
+    uint32_t c = 0, ui = 0;
+    bool live = true;
+    for (int u = blockIdx.x; u < units && live; u += gridDim.x, ++ui) {
+      const ProductUnit t = product_unit(p, u);
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      const uint32_t idesc = idesc_f16(128, (t.cols + 15) / 16 * 16, BF16, t.side == 1, true);
+      // A: 32 bytes along a K-major row, or 16 contraction rows of an M-major slab, per 16 of K
+      const uint32_t a_step = t.side == 1 ? 2048 : 32, a_lbo = t.side == 1 ? C::SLAB : 16;
+      if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
+      tc_fence_after();
+      for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
+        const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+        if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
+        tc_fence_after();
+        const uint32_t s = base + st * C::STAGE;
+#pragma unroll
+        for (int kk = 0; kk < C::BK / 16; ++kk)
+          mma_ss(tmem + ab * 256, sdesc_sw128(s + kk * a_step, a_lbo, 1024),
+                 sdesc_sw128(s + C::A_BYTES + kk * 2048, C::SLAB, 1024), idesc, (ks > t.k0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[st]);
+      }
+      if (live) mma_commit(&acc_full[ab]);
+    }
+    volatile uint32_t never = 0;
+    mma_commit(drain_bar);
+    mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2, ew = warp - 4;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* stg = smem + C::OFF_STG + ew * 4096;
+    uint32_t ui = 0;
+    bool live = true;
+    for (int u = blockIdx.x; u < units && live; u += gridDim.x, ++ui) {
+      const ProductUnit t = product_unit(p, u);
+      const ProductSide& sd = p.s[t.side];
+      const CUtensorMap* tmO = t.side == 0 ? &tmO0 : &tmO1;
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      const int r0 = t.m0 + quarter * 32;
+      live = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], na & 1, kSiteAccFull, abort_flag));
+      if (!live) break;
+      tc_fence_after();
+      const bool f32 = sd.splits > 1;
+      const int cw = f32 ? 32 : 64;             // columns per staged piece of 128 bytes
+      // the two warps of a quarter take the pieces in turn; pieces never cross
+      // the tile's edge (bn is a multiple of 64), TMA clips at the result's
+#pragma unroll 1
+      for (int c0 = half * cw; c0 < t.cols && r0 < sd.M; c0 += 2 * cw) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll 1
+        for (int cc = 0; cc < cw; cc += 32) {
+          uint32_t v[32];
+          tmem_ld_x32(tmem + ab * 256 + c0 + cc + lane_off, v);
+          tmem_wait_ld();
+          reg_fence<32>(v);
+          if (f32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (((cc / 8 + q) ^ (lane & 7)) << 4)) =
+                  pack8<BF16>(reinterpret_cast<const float*>(v) + 8 * q);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(tmO, stg, t.n0 + c0, r0, t.split);
+          bulk_commit();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// out[i] = sum over splits of part[split][i], in split order, n a multiple of 8.
+template <bool BF16>
+__global__ void __launch_bounds__(256) add_splits_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                         void* __restrict__ out) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n / 8; i += stride) {
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(part + s * n) + 2 * i;
+      const float4 u = __ldcs(src), v = __ldcs(src + 1);
+      a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+      a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+    }
+    reinterpret_cast<uint4*>(out)[i] = pack8<BF16>(a);
+  }
+}
+
+}  // namespace sdattn

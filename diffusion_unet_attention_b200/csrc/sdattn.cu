@@ -18,6 +18,7 @@
 
 #include "flash.cuh"
 #include "flash_tf32.cuh"
+#include "gated_ff.cuh"
 #include "layer_norm.cuh"
 #include "qk_stats.cuh"
 #include "row_stats.cuh"
@@ -1150,6 +1151,48 @@ sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, 
     if (r != SDATTN_OK) return r;
   }
   return launch_column_sum(p.part, grid, 2 * desc->C, desc->C, dgamma, dbeta, s) ? SDATTN_OK : SDATTN_ERR_CUDA;
+}
+
+sdattn_status sdattn_gated_ff(const sdattn_ff_desc* desc, const void* X, const void* W, const float* bias, void* Y,
+                              void* stream) {
+  const sdattn_status st = check_ff(desc);
+  if (st != SDATTN_OK) return st;
+  if (desc->T == 0) return SDATTN_OK;
+  if (!X || !W || !Y) return SDATTN_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned16(bias)) return SDATTN_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return desc->dtype == SDATTN_BF16 ? launch_gated<true, false>(desc, X, W, bias, nullptr, Y, nullptr, s)
+                                    : launch_gated<false, false>(desc, X, W, bias, nullptr, Y, nullptr, s);
+}
+
+size_t sdattn_gated_ff_bwd_workspace_bytes(const sdattn_ff_desc* desc) {
+  if (check_ff(desc) != SDATTN_OK) return 0;
+  if (desc->T == 0) return 256;   // nothing is planned; never 0 for a valid desc
+  const int dev = current_device();
+  return plan_ff_bwd(desc, sm_count(dev < 0 ? 0 : dev)).total;
+}
+
+sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, const void* X, const void* W,
+                                  const float* bias, void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  const sdattn_status st = check_ff(desc);
+  if (st != SDATTN_OK) return st;
+  if (!W || !dW || (desc->T > 0 && (!dY || !X || !dX))) return SDATTN_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(W) || !aligned16(dX) || !aligned16(dW) || !aligned16(bias) ||
+      !aligned_to(dbias, 4))
+    return SDATTN_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (desc->T == 0) {   // no rows: the sums are zero
+    if (cudaMemsetAsync(dW, 0, size_t(4) * desc->F * desc->C, s) != cudaSuccess) return SDATTN_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, size_t(8) * desc->F, s) != cudaSuccess) return SDATTN_ERR_CUDA;
+    return SDATTN_OK;
+  }
+  const int dev = current_device();
+  const FFBwdPlan pl = plan_ff_bwd(desc, sm_count(dev < 0 ? 0 : dev));
+  if (!ws || ws_bytes < pl.total) return SDATTN_ERR_WORKSPACE;
+  if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
+  return desc->dtype == SDATTN_BF16 ? launch_ff_bwd<true>(desc, pl, dY, X, W, bias, dX, dW, dbias, ws, s)
+                                    : launch_ff_bwd<false>(desc, pl, dY, X, W, bias, dX, dW, dbias, ws, s);
 }
 
 const char* sdattn_status_string(sdattn_status status) {

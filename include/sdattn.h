@@ -350,6 +350,44 @@ sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, 
                                     const float* gamma, void* dX, float* dgamma, float* dbeta, void* ws,
                                     size_t ws_bytes, void* stream);
 
+/* Shape of one gated feed-forward: X [T][C], W [2F][C] (its first F rows
+ * project to h, its last F to the gate g), Y [T][F], row-major and
+ * contiguous, element type dtype (F16 or BF16).  C and F must be multiples of
+ * 8, at most 65536, and T below 2^27 (SDATTN_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+    int64_t T;        /* rows, >= 0 */
+    int32_t C;        /* input width */
+    int32_t F;        /* output width (per half of the projection) */
+    int32_t dtype;    /* sdattn_dtype of X, W, Y and their gradients */
+} sdattn_ff_desc;
+
+/* The UNet's gated feed-forward in one launch: both halves of the projection,
+ * the activation of sdattn_geglu and the product; the 2F-wide projection is
+ * never stored:
+ *   h = X W[:F]^T + bias[:F],  g = X W[F:]^T + bias[F:],
+ *   Y[t][f] = h[t][f] * g/2 * (1 + erf(g / sqrt(2)))
+ * (16-bit products, fp32 sums and activation, Y rounded once).  X, W: inputs;
+ * bias: float32 [2F] or NULL; Y: output.  T = 0 does nothing. */
+sdattn_status sdattn_gated_ff(const sdattn_ff_desc* desc, const void* X, const void* W, const float* bias, void* Y,
+                              void* stream);
+
+/* Bytes of workspace sdattn_gated_ff_bwd needs on the current device; 0 for an invalid desc. */
+size_t sdattn_gated_ff_bwd_workspace_bytes(const sdattn_ff_desc* desc);
+
+/* Gated feed-forward, backward pass, from the forward's inputs alone (h and g
+ * are computed again).  With GELU(g) = g Phi(g), GELU'(g) = Phi(g) + g phi(g):
+ *   P = [dY GELU(g), dY h GELU'(g)]   [T][2F],
+ *   dX = P W,  dW = P^T X,  dbias = column sums of P.
+ * P is rounded to dtype once, as the products' operand; dbias (float32 [2F])
+ * is summed before that rounding.  dY [T][F], X, W, bias (or NULL): inputs;
+ * dX [T][C], dW [2F][C]: outputs of type dtype, rounded once; dbias: output
+ * or NULL.  With T = 0 dW and dbias are zero-filled.  Every sum has a fixed
+ * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-
+ * owned, overwritten, no state between calls.  Up to five launches. */
+sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, const void* X, const void* W,
+                                  const float* bias, void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 /* Reads and clears this device's error word (synchronises the device).
  * Returns SDATTN_OK, SDATTN_ERR_TIMEOUT, or SDATTN_ERR_CUDA if it cannot be
  * read.  If detail is not NULL it receives a code naming the wait that ran

@@ -59,3 +59,37 @@ def test_python_refuses_cpu_tensors():
         sd.layer_norm(x)
     with pytest.raises(ValueError):
         sd.layer_norm_backward(x, x, torch.zeros(4, 2))
+
+
+def ff(T=64, C=320, F=1280, dtype=0):
+    from diffusion_unet_attention_b200 import _lib
+    return ctypes.byref(_lib.FFDesc(T, C, F, dtype))
+
+
+@pytest.mark.parametrize("kw,status", [(dict(T=-1), 1), (dict(C=0), 1), (dict(F=0), 1), (dict(C=12), 2), (dict(F=20), 2),
+                                       (dict(dtype=2), 2), (dict(T=1 << 27), 2), (dict(C=65544), 2)])
+def test_gated_ff_descriptor(lib, kw, status):
+    d = ff(**kw)
+    assert lib.sdattn_gated_ff(d, OK, OK, OK, OK, None) == status
+    assert lib.sdattn_gated_ff_bwd(d, OK, OK, OK, OK, OK, OK, OK, OK, 1 << 40, None) == status
+    assert lib.sdattn_gated_ff_bwd_workspace_bytes(d) == 0
+
+
+def test_gated_ff_pointers(lib):
+    fwd, bwd = lib.sdattn_gated_ff, lib.sdattn_gated_ff_bwd
+    assert fwd(None, OK, OK, OK, OK, None) == 1
+    assert fwd(ff(), None, OK, OK, OK, None) == 1
+    assert fwd(ff(), OK, OK, OK, None, None) == 1
+    for k in range(4):
+        args = [OFF4 if i == k else OK for i in range(4)]
+        assert fwd(ff(), *args, None) == 3
+    assert fwd(ff(T=0), None, None, None, None, None) == 0
+    assert lib.sdattn_gated_ff_bwd_workspace_bytes(ff(T=0)) > 0
+    need = lib.sdattn_gated_ff_bwd_workspace_bytes(ff())
+    assert need >= 64 * 2560 * 2                              # the projection's gradient in 16 bits
+    assert bwd(ff(), OK, OK, OK, OK, OK, OK, OK, OK, need - 1, None) == 4
+    assert bwd(ff(), OK, OK, OK, OK, OK, OK, OK, None, need, None) == 4
+    assert bwd(ff(), OK, OK, OK, OK, None, OK, OK, OK, need, None) == 1
+    assert bwd(ff(), OK, OK, OK, OK, OK, None, OK, OK, need, None) == 1
+    assert bwd(ff(), OFF4, OK, OK, OK, OK, OK, OK, OK, need, None) == 3
+    assert bwd(ff(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK, need, None) == 3

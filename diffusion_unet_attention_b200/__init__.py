@@ -17,7 +17,9 @@ stored in fp16 (`qk_stats_f16a`, `softmax_av_f16a`).  Beside attention, the
 two specialised UNet kernels of the same section: `group_norm` and `geglu`.
 Around attention, the rest of the transformer block: `layer_norm` with its
 backward pass `layer_norm_backward`, and the gated feed-forward `gated_ff`
-(projections, activation and product in one kernel) with `gated_ff_backward`.
+(projections, activation and product in one kernel) with `gated_ff_backward`,
+and `adapter_linear`, a projection shared by requests with a low-rank adapter
+each.
 
 This module only marshals torch tensors (device memory and streams) into the
 C ABI of libsdattn.so; all arithmetic runs in the CUDA kernels.  There is no
@@ -34,7 +36,7 @@ from . import _lib
 
 __all__ = ["qk_stats", "softmax_av", "flash", "flash_f32o", "flash_tf32", "partially_fused", "qk_scores", "row_stats", "qk_stats_f16a",
            "softmax_av_f16a", "group_norm", "geglu", "wino_filter", "conv3x3_winograd", "wino_workspace_bytes",
-           "layer_norm", "layer_norm_backward", "gated_ff", "gated_ff_backward",
+           "layer_norm", "layer_norm_backward", "gated_ff", "gated_ff_backward", "adapter_linear",
            "device_error", "a_ld", "a16_ld", "workspace_bytes", "SdattnError", "load_library"]
 
 SdattnError = _lib.SdattnError
@@ -566,6 +568,61 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     _call(x.device, "sdattn_gated_ff_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
           dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), ws.numel())
     return dx, dw, db
+
+
+def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+                   down: torch.Tensor | None = None, up: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None):
+    """A projection shared by many requests, each with a low-rank adapter of
+    its own: for request g with i = ids[g],
+
+        y[g] = x[g] w^T + bias + scale[i] * (x[g] down[i]^T) up[i]^T,
+
+    and the projection alone where i is not in 0 .. L-1 (-1 by convention).
+    x [G, ..., C] and w [K, C] (fp16 or bf16), fp32 bias [K] or None; down
+    [L, R, C] and up [L, K, R] of x's dtype, fp32 scale [L] (None: ones), ids
+    [G] int32 on x's device; without ids the plain projection.  C, K and R must
+    be multiples of 8 (pad smaller ranks with zeros once), R at most 256.
+    For requests of different lengths pass their rows as x [T, C] with one id a
+    row.  Returns [G, ..., K]."""
+    if not x.is_cuda or x.dim() < 1:
+        raise ValueError("x must be a CUDA tensor [G, ..., C]")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"dtype {x.dtype} not supported (float16 or bfloat16)")
+    C = x.shape[-1]
+    if w.dim() != 2 or w.shape[1] != C or w.dtype != x.dtype:
+        raise ValueError(f"w must be [K, {C}] of x's dtype")
+    K = w.shape[0]
+    if C < 1 or K < 1:
+        raise ValueError("widths must be at least 1")
+    _same_device(x, w=w, down=down, up=up, scale=scale, ids=ids)
+    T, L, R, rows = x.numel() // C, 0, 0, 1
+    if ids is None:
+        if down is not None or up is not None or scale is not None:
+            raise ValueError("adapters need ids")
+    else:
+        if x.dim() < 2 or ids.shape != x.shape[:1] or ids.dtype != torch.int32:
+            raise ValueError("ids must be int32 [G] for x [G, ..., C]")
+        if down is None or up is None or down.dim() != 3 or down.shape[2] != C:
+            raise ValueError(f"down must be [L, R, {C}]")
+        L, R = down.shape[:2]
+        if up.shape != (L, K, R) or down.dtype != x.dtype or up.dtype != x.dtype:
+            raise ValueError(f"up must be [{L}, {K}, {R}], down and up of x's dtype")
+        if L == 0 or R == 0:                # nothing to add
+            ids = down = up = scale = None
+            L = R = 0
+        else:
+            rows = max(T // max(x.shape[0], 1), 1)
+            scale = _vector(scale, L, x.device, "scale")
+            ids, down, up = _contig(ids), _contig(down), _contig(up)
+    b = _vector(bias, K, x.device, "bias")
+    desc = _lib.AdapterDesc(T, C, K, L, R, rows, _DTYPES[x.dtype])
+    x, w = _contig(x), _contig(w)
+    y = _out(out, x.shape[:-1] + (K,), x.dtype, x.device)
+    _call(x.device, "sdattn_adapter_linear", ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(down),
+          _ptr(up), _ptr(scale), _ptr(ids), y.data_ptr())
+    return y
 
 
 def device_error():

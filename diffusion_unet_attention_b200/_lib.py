@@ -34,6 +34,7 @@ EXPORTS = ("sdattn_a_ld", "sdattn_workspace_bytes", "sdattn_qk_stats", "sdattn_s
            "sdattn_wino_filter_bytes", "sdattn_wino_workspace_bytes", "sdattn_wino_filter", "sdattn_wino_conv3x3",
            "sdattn_layer_norm", "sdattn_layer_norm_bwd_workspace_bytes", "sdattn_layer_norm_bwd",
            "sdattn_gated_ff", "sdattn_gated_ff_bwd_workspace_bytes", "sdattn_gated_ff_bwd",
+           "sdattn_adapter_linear",
            "sdattn_device_error", "sdattn_status_string", "sdattn_version")
 
 
@@ -63,6 +64,12 @@ class LNDesc(ctypes.Structure):
 class FFDesc(ctypes.Structure):
     """sdattn_ff_desc: shape of one gated feed-forward."""
     _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class AdapterDesc(ctypes.Structure):
+    """sdattn_adapter_desc: shape of one projection with adapters."""
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("K", ctypes.c_int32), ("L", ctypes.c_int32),
+                ("R", ctypes.c_int32), ("rows", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class SdattnError(RuntimeError):
@@ -138,6 +145,8 @@ def load(path: str = LIB_PATH):
     lib.sdattn_gated_ff_bwd_workspace_bytes.restype = sz
     lib.sdattn_gated_ff_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdattn_gated_ff_bwd.restype = ctypes.c_int
+    lib.sdattn_adapter_linear.argtypes = [ctypes.POINTER(AdapterDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sdattn_adapter_linear.restype = ctypes.c_int
     lib.sdattn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.sdattn_device_error.restype = ctypes.c_int
     lib.sdattn_status_string.argtypes = [ctypes.c_int]

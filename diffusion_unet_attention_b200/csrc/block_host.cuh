@@ -1,5 +1,6 @@
 // block_host.cuh -- argument checks, plans and launches of the transformer
-// block's operators around attention (layer norm, gated feed-forward).  Included by sdattn.cu
+// block's operators around attention (layer norm, gated feed-forward,
+// projections with adapters).  Included by sdattn.cu
 // after its launch helpers, inside its anonymous namespace.
 #pragma once
 
@@ -331,4 +332,85 @@ sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const 
   if (dbias && !launch_column_sum(db_part, (d->T + 127) / 128 * 4, 2 * d->F, 2 * d->F, dbias, dbias, s))
     return SDATTN_ERR_CUDA;
   return SDATTN_OK;
+}
+
+// --------------------------------------------------------------------------
+// Projection with low-rank adapters (adapter.cuh)
+// --------------------------------------------------------------------------
+sdattn_status check_adapter(const sdattn_adapter_desc* d) {
+  if (!d) return SDATTN_ERR_INVALID_ARG;
+  if (d->T < 0 || d->C < 1 || d->K < 1 || d->L < 0 || d->R < 0 || d->rows < 1 || d->T % d->rows != 0)
+    return SDATTN_ERR_INVALID_ARG;
+  if ((d->L == 0) != (d->R == 0)) return SDATTN_ERR_INVALID_ARG;
+  if (d->dtype != SDATTN_F16 && d->dtype != SDATTN_BF16) return SDATTN_ERR_UNSUPPORTED;
+  // whole 16-byte units along C, K and R, as TMA needs; the bounds keep every
+  // tile count in 32 bits
+  if (d->C % 8 != 0 || d->K % 8 != 0 || d->R % 8 != 0 || d->C > 65536 || d->K > 65536 || d->R > 256 ||
+      d->T >= (int64_t(1) << 27))
+    return SDATTN_ERR_UNSUPPORTED;
+  return SDATTN_OK;
+}
+
+// Columns per tile (a multiple of 16 up to 192): the fewest waves of the
+// longer of a tile's products (2 clocks per column and 64 of C, the adapters'
+// ranks included) and loads (64 bytes per clock and SM), its epilogue beside
+// them, plus one epilogue at the end.
+int plan_adapter(const sdattn_adapter_desc* d, int rc, int nsm) {
+  const int64_t rts = (d->T + 127) / 128;
+  const double ksteps = (d->C + 63) / 64;
+  int best_bn = sdattn::AdapterCfg::BN;
+  double best = 1e300;
+  for (int bn = sdattn::AdapterCfg::BN; bn >= 16; bn -= 16) {
+    const int64_t tiles = rts * ((d->K + bn - 1) / bn);
+    const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
+    const double tile = std::max(ksteps * std::max(2.0 * (bn + rc), 2.0 * (128 + bn + rc)), 8.0 * bn);
+    const double cost = waves * tile + 8.0 * bn;
+    if (cost < best) {
+      best = cost;
+      best_bn = bn;
+    }
+  }
+  return best_bn;
+}
+
+template <bool BF16>
+sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const void* W, const float* bias,
+                             const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
+                             cudaStream_t s) {
+  const int dev = current_device();
+  if (dev < 0) return SDATTN_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  const uint64_t T = d->T, C = d->C, K = d->K, L = d->L, R = d->R;
+  sdattn::AdapterParams p;
+  p.bias = bias;
+  p.ids = ids;
+  p.scale = scale;
+  p.Y = Y;
+  p.T = static_cast<int>(T);
+  p.K = d->K;
+  p.L = ids ? d->L : 0;
+  p.rows = d->rows;
+  p.rc = std::max(16, std::min(64, (d->R + 15) / 16 * 16));
+  p.chunks = std::max(1, (d->R + 63) / 64);
+  p.bn = plan_adapter(d, ids ? p.rc : 0, nsm);
+  p.tm = 128;
+  p.rts = static_cast<int>((T + p.tm - 1) / p.tm);
+  p.nts = (d->K + p.bn - 1) / p.bn;
+  p.ksteps = (d->C + 63) / 64;
+  const CUtensorMapDataType dt = elem16(d->dtype);
+  CUtensorMap mx, mw, md, mu;
+  if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mw, W, dt, C, K, 1, C * 2, K * C * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
+  if (ids) {
+    if (!make_map_3d(&md, D, dt, C, R, L, C * 2, R * C * 2, 64, static_cast<uint32_t>(p.rc))) return SDATTN_ERR_CUDA;
+    if (!make_map_3d(&mu, U, dt, R, K, L, R * 2, K * R * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
+  } else {
+    md = mu = mw;   // never read
+  }
+  auto kern = sdattn::adapter_kernel<BF16>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kern, sdattn::AdapterCfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
+  const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.nts));
+  return launch(kern, grid, sdattn::AdapterCfg::NTHREADS, sdattn::AdapterCfg::SMEM, s, mx, mw, md, mu, p) ? SDATTN_OK
+                                                                                                          : SDATTN_ERR_CUDA;
 }

@@ -16,6 +16,7 @@
 
 #include "sdattn.h"
 
+#include "adapter.cuh"
 #include "flash.cuh"
 #include "flash_tf32.cuh"
 #include "gated_ff.cuh"
@@ -1193,6 +1194,22 @@ sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, co
   if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
   return desc->dtype == SDATTN_BF16 ? launch_ff_bwd<true>(desc, pl, dY, X, W, bias, dX, dW, dbias, ws, s)
                                     : launch_ff_bwd<false>(desc, pl, dY, X, W, bias, dX, dW, dbias, ws, s);
+}
+
+sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
+                                    const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
+                                    void* stream) {
+  const sdattn_status st = check_adapter(desc);
+  if (st != SDATTN_OK) return st;
+  if (desc->T == 0) return SDATTN_OK;
+  if (!X || !W || !Y) return SDATTN_ERR_INVALID_ARG;
+  if (ids ? desc->L == 0 || !D || !U : D || U || scale) return SDATTN_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(bias) || !aligned16(D) || !aligned16(U) || !aligned16(Y) ||
+      !aligned_to(scale, 4) || !aligned_to(ids, 4))
+    return SDATTN_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return desc->dtype == SDATTN_BF16 ? launch_adapter<true>(desc, X, W, bias, D, U, scale, ids, Y, s)
+                                    : launch_adapter<false>(desc, X, W, bias, D, U, scale, ids, Y, s);
 }
 
 const char* sdattn_status_string(sdattn_status status) {

@@ -388,6 +388,37 @@ sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, co
                                   const float* bias, void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* Shape of one projection with adapters: X [T][C], W [K][C], down matrices D
+ * [L][R][C], up matrices U [L][K][R], Y [T][K], row-major and contiguous,
+ * element type dtype (F16 or BF16).  Rows rows*r .. rows*r + rows - 1 belong
+ * to request r.  C, K and R must be multiples of 8 (adapters of smaller or
+ * different ranks are padded with zero rows of D and columns of U), C and K at
+ * most 65536, R at most 256 and T below 2^27 (SDATTN_ERR_UNSUPPORTED
+ * otherwise); T must be a multiple of rows. */
+typedef struct {
+    int64_t T;        /* rows, >= 0 */
+    int32_t C, K;     /* input and output width */
+    int32_t L, R;     /* adapters and their rank; 0 and 0 for the plain projection */
+    int32_t rows;     /* rows per request, >= 1 */
+    int32_t dtype;    /* sdattn_dtype of X, W, D, U and Y */
+} sdattn_adapter_desc;
+
+/* A projection shared by many requests, each with a low-rank adapter of its
+ * own, in one launch: with i = ids[t / rows],
+ *   Y[t] = X[t] W^T + bias + scale[i] (X[t] D[i]^T) U[i]^T     if 0 <= i < L,
+ *   Y[t] = X[t] W^T + bias                                     otherwise
+ * (16-bit products with fp32 sums; scale[i] X D[i]^T is rounded to dtype once,
+ * as the second product's operand; Y is rounded once).  X, W: inputs; bias:
+ * float32 [K] or NULL; ids: int32 [T / rows] in device memory, or NULL for the
+ * plain projection (then D, U and scale must be NULL too); scale: float32 [L]
+ * or NULL (ones).  Requests may name adapters in any order and share them;
+ * the call is cheapest when neighbouring requests share one, since each
+ * distinct adapter among a tile's 128 rows costs it one more small product.
+ * T = 0 does nothing. */
+sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
+                                    const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
+                                    void* stream);
+
 /* Reads and clears this device's error word (synchronises the device).
  * Returns SDATTN_OK, SDATTN_ERR_TIMEOUT, or SDATTN_ERR_CUDA if it cannot be
  * read.  If detail is not NULL it receives a code naming the wait that ran

@@ -93,3 +93,27 @@ def test_gated_ff_pointers(lib):
     assert bwd(ff(), OK, OK, OK, OK, OK, None, OK, OK, need, None) == 1
     assert bwd(ff(), OFF4, OK, OK, OK, OK, OK, OK, OK, need, None) == 3
     assert bwd(ff(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK, need, None) == 3
+
+
+def ad(T=64, C=320, K=320, L=2, R=16, rows=32, dtype=0):
+    from diffusion_unet_attention_b200 import _lib
+    return ctypes.byref(_lib.AdapterDesc(T, C, K, L, R, rows, dtype))
+
+
+@pytest.mark.parametrize("kw,status", [(dict(T=-1), 1), (dict(C=0), 1), (dict(K=0), 1), (dict(L=-1), 1), (dict(rows=0), 1),
+                                       (dict(rows=48), 1), (dict(L=0), 1), (dict(R=0), 1), (dict(C=12), 2), (dict(K=20), 2),
+                                       (dict(R=4), 2), (dict(R=264), 2), (dict(dtype=2), 2), (dict(T=1 << 27), 2)])
+def test_adapter_descriptor(lib, kw, status):
+    assert lib.sdattn_adapter_linear(ad(**kw), OK, OK, OK, OK, OK, OK, OK, OK, None) == status
+
+
+def test_adapter_pointers(lib):
+    f = lib.sdattn_adapter_linear
+    assert f(None, OK, OK, OK, OK, OK, OK, OK, OK, None) == 1
+    for k in (0, 1, 3, 4, 7):                      # X, W, D, U, Y
+        assert f(ad(), *[None if i == k else OK for i in range(8)], None) == 1
+        assert f(ad(), *[OFF4 if i == k else OK for i in range(8)], None) == 3
+    assert f(ad(), OK, OK, OK, OK, OK, OK, None, OK, None) == 1              # adapters without ids
+    assert f(ad(L=0, R=0), OK, OK, OK, OK, OK, OK, OK, OK, None) == 1        # ids without adapters
+    assert f(ad(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK, None) == 3
+    assert f(ad(T=0), *[None] * 8, None) == 0

@@ -28,6 +28,7 @@ CPU fallback: calls fail if the library or a CUDA device is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -425,22 +426,17 @@ def wino_workspace_bytes(N: int, C: int, K: int, H: int, W: int, dtype=torch.flo
     return int(_lib_handle().sdattn_wino_workspace_bytes(ctypes.byref(_conv_desc(N, C, K, H, W, dtype))))
 
 
-def _call(device: torch.device, fn: str, *args) -> None:
-    """Calls the library's `fn` with `device` current, the stream (the last
-    argument) being the device's current one; raises on a status."""
-    f = getattr(_lib_handle(), fn)
-    if device.index == torch.cuda.current_device():
-        st = f(*args, _stream(device))
+def _call(device: torch.device, fn, *args) -> None:
+    """Calls the library's function `fn` with `device` current, the stream (the
+    last argument) being the device's current one; raises on a status."""
+    at = device.index
+    if at == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(at))
     else:
         with torch.cuda.device(device):
-            st = f(*args, _stream(device))
-    _lib.check(fn, st)
-
-
-def _query(device: torch.device, fn: str, *args) -> int:
-    """The library's size query `fn`, asked with `device` current."""
-    with torch.cuda.device(device):
-        return int(getattr(_lib_handle(), fn)(*args))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(at))
+    if st != 0:
+        _lib.check(fn.__name__, st)
 
 
 def _same_device(x: torch.Tensor, **others) -> None:
@@ -450,39 +446,58 @@ def _same_device(x: torch.Tensor, **others) -> None:
 
 
 def _vector(t: torch.Tensor | None, n: int, device: torch.device, name: str) -> torch.Tensor | None:
-    """A parameter vector as contiguous fp32 [n] on `device`."""
+    """A parameter vector as contiguous fp32 [n] on `device`, on a 16-byte boundary."""
     if t is None:
         return None
-    if t.shape != (n,):
+    if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be [{n}]")
-    t = _contig(t.to(device=device, dtype=torch.float32))
-    return t if t.data_ptr() % 16 == 0 else t.clone()      # a slice of a larger vector
+    if t.dtype is not torch.float32 or t.device != device:
+        t = t.to(device=device, dtype=torch.float32)
+    if not t.is_contiguous() or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)      # a slice of a larger tensor
+    return t
 
 
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _out(out: torch.Tensor | None, shape, dtype: torch.dtype, device: torch.device, name: str = "out") -> torch.Tensor:
+def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
+    """The output: `out` if it fits, else a new tensor of x's dtype."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
+        return x.new_empty(shape)
+    if out.shape != shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {x.dtype} {list(shape)} on {x.device}")
     return out
+
+
+# Descriptors and workspace sizes follow from the shapes alone, so the last
+# few are kept: building one again costs more of the host's time than the rest
+# of its call.
+@functools.lru_cache(maxsize=256)
+def _shape(kind, *fields):
+    return ctypes.byref(kind(*fields))
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(device: torch.device, fn: str, kind, *fields) -> int:
+    with torch.cuda.device(device):
+        return int(getattr(_lib_handle(), fn)(_shape(kind, *fields)))
 
 
 _LN_DTYPES = {**_DTYPES, torch.float32: _lib.SDATTN_F32}
 
 
-def _ln_desc(x: torch.Tensor, eps: float) -> _lib.LNDesc:
+def _ln_fields(x: torch.Tensor, eps: float):
     if not x.is_cuda or x.dim() < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
-    if x.dtype not in _LN_DTYPES:
+    dt = _LN_DTYPES.get(x.dtype)
+    if dt is None:
         raise TypeError(f"dtype {x.dtype} not supported (float16, bfloat16 or float32)")
     C = x.shape[-1]
     if C < 1:
         raise ValueError("rows must have at least one value")
-    return _lib.LNDesc(x.numel() // C, C, _LN_DTYPES[x.dtype], float(eps))
+    return x.numel() // C, C, dt, float(eps)
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -492,12 +507,14 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
 
     With `return_stats` returns (y, stats), stats [..., 2] fp32 = (mean,
     1 / sqrt(var + eps)) of every row, as `layer_norm_backward` takes it."""
-    desc = _ln_desc(x, eps)
-    g, b = _vector(gamma, desc.C, x.device, "gamma"), _vector(beta, desc.C, x.device, "beta")
+    fields = _ln_fields(x, eps)
+    dev, C = x.device, fields[1]
+    g, b = _vector(gamma, C, dev, "gamma"), _vector(beta, C, dev, "beta")
     x = _contig(x)
-    y = _out(out, x.shape, x.dtype, x.device)
-    stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device) if return_stats else None
-    _call(x.device, "sdattn_layer_norm", ctypes.byref(desc), x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
+    y = torch.empty_like(x) if out is None else _out(out, x, x.shape)
+    stats = x.new_empty(x.shape[:-1] + (2,), dtype=torch.float32) if return_stats else None
+    _call(dev, _lib_handle().sdattn_layer_norm, _shape(_lib.LNDesc, *fields), x.data_ptr(), _ptr(g), _ptr(b),
+          y.data_ptr(), _ptr(stats))
     return (y, stats) if return_stats else y
 
 
@@ -505,27 +522,28 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     """Gradients of `layer_norm`: (dx, dgamma, dbeta) from dy (x's shape and
     dtype), the forward's x and stats, and gamma.  dx has x's dtype, dgamma and
     dbeta are fp32 [C]; repeated calls give identical bits."""
-    desc = _ln_desc(x, 0.0)
+    fields = _ln_fields(x, 0.0)
+    dev, C = x.device, fields[1]
     _same_device(x, dy=dy, stats=stats)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must match x in shape and dtype")
     if stats.shape != x.shape[:-1] + (2,) or stats.dtype != torch.float32:
         raise ValueError("stats must be layer_norm's fp32 [..., 2]")
-    g = _vector(gamma, desc.C, x.device, "gamma")
+    g = _vector(gamma, C, dev, "gamma")
     dy, x, stats = _contig(dy), _contig(x), _contig(stats)
-    dx = torch.empty_like(x)
-    dgb = torch.empty((2, desc.C), dtype=torch.float32, device=x.device)
-    ws = torch.empty(_query(x.device, "sdattn_layer_norm_bwd_workspace_bytes", ctypes.byref(desc)), dtype=torch.uint8,
-                     device=x.device)
-    _call(x.device, "sdattn_layer_norm_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
-          dx.data_ptr(), dgb[0].data_ptr(), dgb[1].data_ptr(), ws.data_ptr(), ws.numel())
-    return dx, dgb[0], dgb[1]
+    dx, dg, db = torch.empty_like(x), x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
+    need = _bytes(dev, "sdattn_layer_norm_bwd_workspace_bytes", _lib.LNDesc, *fields)
+    ws = x.new_empty(need, dtype=torch.uint8)
+    _call(dev, _lib_handle().sdattn_layer_norm_bwd, _shape(_lib.LNDesc, *fields), dy.data_ptr(), x.data_ptr(),
+          stats.data_ptr(), _ptr(g), dx.data_ptr(), dg.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
+    return dx, dg, db
 
 
-def _ff_desc(x: torch.Tensor, w: torch.Tensor) -> _lib.FFDesc:
+def _ff_fields(x: torch.Tensor, w: torch.Tensor):
     if not x.is_cuda or x.dim() < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
-    if x.dtype not in _DTYPES:
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
         raise TypeError(f"dtype {x.dtype} not supported (float16 or bfloat16)")
     C = x.shape[-1]
     if w.dim() != 2 or w.shape[1] != C or w.shape[0] % 2 or w.dtype != x.dtype:
@@ -533,7 +551,7 @@ def _ff_desc(x: torch.Tensor, w: torch.Tensor) -> _lib.FFDesc:
     _same_device(x, w=w)
     if C < 1 or w.shape[0] < 2:
         raise ValueError("widths must be at least 1")
-    return _lib.FFDesc(x.numel() // C, C, w.shape[0] // 2, _DTYPES[x.dtype])
+    return x.numel() // C, C, w.shape[0] // 2, dt
 
 
 def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None):
@@ -542,11 +560,12 @@ def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
 
     x [..., C] and w [2F, C] (fp16 or bf16), fp32 bias [2F] or None; returns
     [..., F].  C and F must be multiples of 8."""
-    desc = _ff_desc(x, w)
-    b = _vector(bias, 2 * desc.F, x.device, "bias")
+    fields = _ff_fields(x, w)
+    b = _vector(bias, 2 * fields[2], x.device, "bias")
     x, w = _contig(x), _contig(w)
-    y = _out(out, x.shape[:-1] + (desc.F,), x.dtype, x.device)
-    _call(x.device, "sdattn_gated_ff", ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
+    y = _out(out, x, x.shape[:-1] + (fields[2],))
+    _call(x.device, _lib_handle().sdattn_gated_ff, _shape(_lib.FFDesc, *fields), x.data_ptr(), w.data_ptr(), _ptr(b),
+          y.data_ptr())
     return y
 
 
@@ -555,18 +574,19 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     forward's inputs (the projection is computed again).  dx and dw have x's
     dtype; dbias is fp32 [2F], or None without a bias.  Repeated calls give
     identical bits."""
-    desc = _ff_desc(x, w)
+    fields = _ff_fields(x, w)
+    dev, F = x.device, fields[2]
     _same_device(x, dy=dy)
-    if dy.shape != x.shape[:-1] + (desc.F,) or dy.dtype != x.dtype:
-        raise ValueError(f"dy must be x.shape[:-1] + ({desc.F},) of x's dtype")
-    b = _vector(bias, 2 * desc.F, x.device, "bias")
+    if dy.shape != x.shape[:-1] + (F,) or dy.dtype != x.dtype:
+        raise ValueError(f"dy must be x.shape[:-1] + ({F},) of x's dtype")
+    b = _vector(bias, 2 * F, dev, "bias")
     dy, x, w = _contig(dy), _contig(x), _contig(w)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
-    db = torch.empty(2 * desc.F, dtype=torch.float32, device=x.device) if bias is not None else None
-    ws = torch.empty(_query(x.device, "sdattn_gated_ff_bwd_workspace_bytes", ctypes.byref(desc)), dtype=torch.uint8,
-                     device=x.device)
-    _call(x.device, "sdattn_gated_ff_bwd", ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
-          dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), ws.numel())
+    db = x.new_empty(2 * F, dtype=torch.float32) if bias is not None else None
+    need = _bytes(dev, "sdattn_gated_ff_bwd_workspace_bytes", _lib.FFDesc, *fields)
+    ws = x.new_empty(need, dtype=torch.uint8)
+    _call(dev, _lib_handle().sdattn_gated_ff_bwd, _shape(_lib.FFDesc, *fields), dy.data_ptr(), x.data_ptr(),
+          w.data_ptr(), _ptr(b), dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), need)
     return dx, dw, db
 
 
@@ -617,10 +637,10 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
             scale = _vector(scale, L, x.device, "scale")
             ids, down, up = _contig(ids), _contig(down), _contig(up)
     b = _vector(bias, K, x.device, "bias")
-    desc = _lib.AdapterDesc(T, C, K, L, R, rows, _DTYPES[x.dtype])
     x, w = _contig(x), _contig(w)
-    y = _out(out, x.shape[:-1] + (K,), x.dtype, x.device)
-    _call(x.device, "sdattn_adapter_linear", ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(down),
+    y = _out(out, x, x.shape[:-1] + (K,))
+    _call(x.device, _lib_handle().sdattn_adapter_linear,
+          _shape(_lib.AdapterDesc, T, C, K, L, R, rows, _DTYPES[x.dtype]), x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(down),
           _ptr(up), _ptr(scale), _ptr(ids), y.data_ptr())
     return y
 

@@ -32,17 +32,48 @@
 
 namespace sdattn {
 
-// Phi(g) and exp(-g^2 / 2) by the same approximation as gelu_erf.
-__device__ __forceinline__ void normal_cdf(float g, float& cdf, float& bell) {
-  constexpr float kP = 0.3275911f, kA1 = 0.254829592f, kA2 = -0.284496736f, kA3 = 1.421413741f,
-                  kA4 = -1.453152027f, kA5 = 1.061405429f;
-  constexpr float kRsqrt2 = 0.7071067811865476f, kL2E = 1.4426950408889634f;
-  const float x = fabsf(g) * kRsqrt2;
-  float t;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(kP, x, 1.f)));
-  bell = ex2_approx(-x * x * kL2E);
-  const float half_erfc = 0.5f * t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, kA5, kA4), kA3), kA2), kA1) * bell;
-  cdf = g >= 0.f ? 1.f - half_erfc : half_erfc;
+// GELU of a pair of gates on packed fp32 pairs (half the instructions of two
+// scalars), with gelu_erf's approximation (Abramowitz and Stegun 7.1.26):
+//   q = erfc(|g| / sqrt 2) / 2 = t (a1 + t (a2 + ...)) / 2 exp(-g^2 / 2),  t = 1 / (1 + p |g| / sqrt 2)
+//   Phi(g) = 1 - q for g >= 0 and q below,  so  GELU(g) = max(g, 0) - |g| q.
+struct GeluPair {
+  uint64_t gelu;   // g Phi(g)
+  uint64_t nq;     // -q
+  uint64_t bell;   // exp(-g^2 / 2)
+};
+
+__device__ __forceinline__ GeluPair gelu_pair(uint64_t g) {
+  constexpr float kP = 0.3275911f * 0.7071067811865476f, kA1 = -0.5f * 0.254829592f, kA2 = 0.5f * 0.284496736f,
+                  kA3 = -0.5f * 1.421413741f, kA4 = 0.5f * 1.453152027f, kA5 = -0.5f * 1.061405429f;
+  constexpr float kE = -0.5f * 1.4426950408889634f;
+  const auto both = [](float c) { return f2_pack(c, c); };
+  float g0, g1, d0, d1, e0, e1, t0, t1;
+  f2_unpack(g, g0, g1);
+  // q is 0 far below 64: the bound keeps an infinite gate from meeting it
+  const uint64_t mag = f2_pack(fminf(fabsf(g0), 64.f), fminf(fabsf(g1), 64.f));
+  f2_unpack(f2_fma(mag, both(kP), both(1.f)), d0, d1);
+  f2_unpack(f2_mul(f2_mul(g, g), both(kE)), e0, e1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(d1));
+  GeluPair r;
+  r.bell = f2_pack(ex2_approx(e0), ex2_approx(e1));
+  const uint64_t t = f2_pack(t0, t1);
+  uint64_t y = f2_fma(t, both(kA5), both(kA4));
+  y = f2_fma(t, y, both(kA3));
+  y = f2_fma(t, y, both(kA2));
+  y = f2_fma(t, y, both(kA1));
+  r.nq = f2_mul(f2_mul(t, y), r.bell);
+  r.gelu = f2_fma(mag, r.nq, f2_pack(fmaxf(g0, 0.f), fmaxf(g1, 0.f)));
+  return r;
+}
+
+// GELU'(g) = Phi(g) + g phi(g), Phi = 1/2 + (1/2 - q) with g's sign.
+__device__ __forceinline__ uint64_t gelu_slope_pair(uint64_t g, const GeluPair& a) {
+  float g0, g1, s0, s1;
+  f2_unpack(g, g0, g1);
+  f2_unpack(f2_add(a.nq, f2_pack(0.5f, 0.5f)), s0, s1);
+  const uint64_t s = f2_add(f2_pack(copysignf(s0, g0), copysignf(s1, g1)), f2_pack(0.5f, 0.5f));
+  return f2_fma(f2_mul(g, f2_pack(0.3989422804014327f, 0.3989422804014327f)), a.bell, s);
 }
 
 // Sums v[i] over the warp's lanes for N columns at once (N a power of two up
@@ -102,27 +133,30 @@ struct GatedParams {
 template <bool BWD, bool BF16>
 __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t* g, const float* bh, int F,
                                                const uint4& dy, float* o0, float* o1) {
-  float b[16], d[8];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int src = 4 * (q & 1) + (q < 2 ? 0 : F);   // of h, then of g
-    const float4 v = bh != nullptr ? __ldg(reinterpret_cast<const float4*>(bh + src)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    b[4 * q] = v.x;
-    b[4 * q + 1] = v.y;
-    b[4 * q + 2] = v.z;
-    b[4 * q + 3] = v.w;
-  }
+  float d[8];
   if constexpr (BWD) unpack8<BF16>(dy, d);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float hv = __uint_as_float(h[e]) + b[e], gv = __uint_as_float(g[e]) + b[8 + e];
-    if constexpr (BWD) {
-      float cdf, bell;
-      normal_cdf(gv, cdf, bell);
-      o0[e] = d[e] * (gv * cdf);
-      o1[e] = d[e] * (hv * fmaf(gv * 0.3989422804014327f, bell, cdf));
-    } else {
-      o0[e] = hv * gelu_erf(gv);
+  for (int q = 0; q < 2; ++q) {
+    float4 bv = make_float4(0.f, 0.f, 0.f, 0.f), gv = bv;
+    if (bh != nullptr) {
+      bv = __ldg(reinterpret_cast<const float4*>(bh) + q);
+      gv = __ldg(reinterpret_cast<const float4*>(bh + F) + q);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = 4 * q + 2 * k;
+      const uint64_t hp = f2_add(f2_pack(__uint_as_float(h[e]), __uint_as_float(h[e + 1])),
+                                 k ? f2_pack(bv.z, bv.w) : f2_pack(bv.x, bv.y));
+      const uint64_t gp = f2_add(f2_pack(__uint_as_float(g[e]), __uint_as_float(g[e + 1])),
+                                 k ? f2_pack(gv.z, gv.w) : f2_pack(gv.x, gv.y));
+      const GeluPair a = gelu_pair(gp);
+      if constexpr (BWD) {
+        const uint64_t dp = f2_pack(d[e], d[e + 1]);
+        f2_unpack(f2_mul(dp, a.gelu), o0[e], o0[e + 1]);
+        f2_unpack(f2_mul(f2_mul(dp, hp), gelu_slope_pair(gp, a)), o1[e], o1[e + 1]);
+      } else {
+        f2_unpack(f2_mul(hp, a.gelu), o0[e], o0[e + 1]);
+      }
     }
   }
 }

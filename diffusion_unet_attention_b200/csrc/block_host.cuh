@@ -174,27 +174,37 @@ CUtensorMapDataType elem16(int dtype) {
   return dtype == SDATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// Columns of h per tile (a multiple of 16 up to 128): the fewest waves of the
-// longest of a tile's products (2 clocks per column pair and 64 of C), loads
-// (64 bytes per clock and SM) and epilogue, plus one tile's epilogue at the
-// end.  Many rows give whole 128-column tiles; few rows narrower ones, until
-// there is about one tile per SM.
-int plan_gated(const sdattn_ff_desc* d, int nsm) {
-  const int64_t rts = (d->T + 127) / 128;
+// Pairs of CTAs on tiles of 256 rows by 128 columns of h, or single CTAs on
+// 128 rows by hn columns (a multiple of 16 up to 128): the fewest waves of the
+// longest of a tile's products (2 clocks per accumulator column and 64 of C),
+// loads (45 bytes per clock and SM, measured with the epilogue left out) and
+// epilogue, plus one tile's epilogue at the end.  Many rows take pairs, which
+// read W's tile once for 256 rows; few rows narrower tiles, until there is
+// about one per SM.
+struct GatedPlan {
+  bool pair;
+  int hn;
+};
+
+GatedPlan plan_gated(const sdattn_ff_desc* d, bool backward, int nsm) {
   const double ksteps = (d->C + 63) / 64;
-  int best_hn = 128;
-  double best = 1e300;
+  const double epi = backward ? 40.0 : 20.0;      // clocks per column of a 128-row tile
+  auto cost = [&](int64_t tiles, int64_t slots, int hn, double bytes) {
+    const double waves = static_cast<double>((tiles + slots - 1) / slots);
+    return waves * std::max(ksteps * std::max(4.0 * hn, bytes / 45.0), epi * hn) + epi * hn;
+  };
+  GatedPlan best{true, 128};
+  double least = 1e300;
+  if (d->T > 128) least = cost((d->T + 255) / 256 * ((d->F + 127) / 128), nsm / 2, 128, 16384.0 + 16384.0);
   for (int hn = 128; hn >= 16; hn -= 16) {
-    const int64_t tiles = rts * ((d->F + hn - 1) / hn);
-    const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
-    const double tile = std::max(ksteps * std::max(4.0 * hn, (16384.0 + 256.0 * hn) / 64.0), 24.0 * hn);
-    const double cost = waves * tile + 24.0 * hn;
-    if (cost < best) {
-      best = cost;
-      best_hn = hn;
+    // the narrow form's stores cost it about half as much again
+    const double c = cost((d->T + 127) / 128 * ((d->F + hn - 1) / hn), nsm, hn, 16384.0 + 256.0 * hn) + 0.5 * epi * hn;
+    if (c < least) {
+      least = c;
+      best = {false, hn};
     }
   }
-  return best_hn;
+  return best;
 }
 
 template <bool BF16, bool BWD>
@@ -211,8 +221,9 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   p.part = part;
   p.T = static_cast<int>(T);
   p.F = d->F;
-  p.hn = plan_gated(d, nsm);
-  p.rts = static_cast<int>((T + 127) / 128);
+  const GatedPlan plan = plan_gated(d, BWD, nsm);
+  p.hn = plan.hn;
+  p.rts = static_cast<int>(plan.pair ? (T + 255) / 256 : (T + 127) / 128);
   p.fts = (d->F + p.hn - 1) / p.hn;
   p.ksteps = (d->C + 63) / 64;
   const CUtensorMapDataType dt = elem16(d->dtype);
@@ -220,16 +231,23 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 128)) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, F, 2, C * 2, F * C * 2, 64, static_cast<uint32_t>(p.hn))) return SDATTN_ERR_CUDA;
   const uint64_t ldy = BWD ? 4 * F : 2 * F;   // bytes of a row of y, or of P = [dh, dg]
-  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, 64, 32)) return SDATTN_ERR_CUDA;
-  const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.fts));
-  constexpr int smem = sdattn::GatedSmem<BWD>::BYTES;
-  auto run = [&](auto kern, std::atomic<uint64_t>& done) {
+  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return SDATTN_ERR_CUDA;
+  const int64_t tiles = int64_t(p.rts) * p.fts;
+  if (plan.pair) {
+    auto kern = sdattn::gated_kernel<BF16, BWD, true>;
+    constexpr int smem = sdattn::GatedSmem<BWD, true>::BYTES;
+    static std::atomic<uint64_t> done{0};
     if (!ensure_smem(kern, smem, done, dev)) return SDATTN_ERR_CUDA;
-    return launch(kern, grid, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
-  };
-  static std::atomic<uint64_t> done_full{0}, done_part{0};
-  return p.hn == 128 ? run(sdattn::gated_kernel<BF16, BWD, true>, done_full)
-                     : run(sdattn::gated_kernel<BF16, BWD, false>, done_part);
+    const int grid = static_cast<int>(std::min<int64_t>(nsm / 2, tiles)) * 2;
+    return launch_cluster(kern, grid, 2, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+  }
+  auto kern = sdattn::gated_kernel<BF16, BWD, false>;
+  constexpr int smem = sdattn::GatedSmem<BWD, false>::BYTES;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kern, smem, done, dev)) return SDATTN_ERR_CUDA;
+  const int grid = static_cast<int>(std::min<int64_t>(nsm, tiles));
+  return launch(kern, grid, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 // dx = P W and dW = P^T x: tiles, splits and where their partials lie.
@@ -263,7 +281,7 @@ FFBwdPlan plan_ff_bwd(const sdattn_ff_desc* d, int nsm) {
   size_t at = 0;
   auto place = [&](size_t bytes) { at += (bytes + 255) / 256 * 256; return bytes; };
   pl.p_bytes = place(static_cast<size_t>(d->T) * 2 * d->F * 2);
-  pl.db_bytes = place(static_cast<size_t>((d->T + 127) / 128) * 4 * 2 * d->F * 4);
+  pl.db_bytes = place(static_cast<size_t>((d->T + 31) / 32) * 2 * d->F * 4);
   for (int i = 0; i < 2; ++i) {
     sdattn::ProductSide& s = pl.pp.s[i];
     s.splits = 1;
@@ -329,7 +347,7 @@ sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const 
     const int g = static_cast<int>(std::min<int64_t>((n / 8 + 255) / 256, int64_t(nsm) * 8));
     if (!launch(sdattn::add_splits_kernel<BF16>, g, 256, 0, s, parts[i], sd.splits, n, outs[i])) return SDATTN_ERR_CUDA;
   }
-  if (dbias && !launch_column_sum(db_part, (d->T + 127) / 128 * 4, 2 * d->F, 2 * d->F, dbias, dbias, s))
+  if (dbias && !launch_column_sum(db_part, (d->T + 31) / 32, 2 * d->F, 2 * d->F, dbias, dbias, s))
     return SDATTN_ERR_CUDA;
   return SDATTN_OK;
 }

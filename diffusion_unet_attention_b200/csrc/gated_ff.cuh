@@ -96,52 +96,113 @@ __device__ __forceinline__ float warp_column_sums(float* v, int lane) {
   return t;
 }
 
+// ---------------------------------------------------------------------------
+// CTA pairs (cta_group::2): the two CTAs of a cluster, on neighbouring SMs,
+// run one tcgen05.mma of twice the rows.  Each holds its own 128 rows of A and
+// half of B's rows, so a tile of 256 rows reads B from L2 once instead of
+// twice.  The even CTA (the leader) issues the MMAs; barriers that the other
+// CTA signals are addressed in the leader's shared memory.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+  return remote;
+}
+
+// A TMA load into this CTA's shared memory that signals the leader's barrier.
+__device__ __forceinline__ void tma_load_3d_pair(void* sdst, const CUtensorMap* map, int x, int y, int z,
+                                                 uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(sdst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_result, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_result)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, issued by the leader.
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives once on the barrier at this offset in both CTAs when every MMA the
+// elected thread issued so far has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 struct GatedCfg {
   static constexpr int BK = 64;                     // columns of C per stage
   static constexpr int A_BYTES = 128 * 128;         // 128 rows of x
   static constexpr int HN = 128;                    // most columns of h (and of g) per tile
-  static constexpr int STAGE = A_BYTES + 2 * HN * 128;
-  static constexpr int NTHREADS = 384;              // TMA, MMA, two idle warps, eight epilogue warps
+  static constexpr int EPI = 16;                    // epilogue warps
+  static constexpr int NTHREADS = (4 + EPI) * 32;   // TMA, MMA, bias, one idle warp, epilogue
   static constexpr uint32_t TMEM_COLS = 512;        // two accumulators of 2 HN columns
 };
 
-template <bool BWD>
+// PAIR: a CTA holds its 128 rows of x and the h or the g half of W's tile.
+template <bool BWD, bool PAIR>
 struct GatedSmem {
-  static constexpr int STAGES = BWD ? 3 : 4;
-  static constexpr int WSTG = BWD ? 8192 : 4096;    // an epilogue warp's staged output: 32 rows x 64 columns of y, or of dh and of dg
-  static constexpr int OFF_STG = STAGES * GatedCfg::STAGE;
-  static constexpr int OFF_BAR = OFF_STG + 8 * WSTG;
-  static constexpr int NBAR = 2 * STAGES + 4 + 1;
+  static constexpr int STAGE = GatedCfg::A_BYTES + (PAIR ? 1 : 2) * GatedCfg::HN * 128;
+  static constexpr int STAGES = PAIR && !BWD ? 5 : 4;
+  // an epilogue warp's staged output (PAIR): 32 rows x 32 columns of y, or of dh and of dg
+  static constexpr int WSTG = PAIR ? (BWD ? 4096 : 2048) : 0;
+  static constexpr int OFF_STG = STAGES * STAGE;
+  static constexpr int OFF_BIAS = OFF_STG + GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
+  static constexpr int OFF_BAR = OFF_BIAS + 2 * 2 * GatedCfg::HN * 4;
+  static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;
   static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory budget");
 };
 
 struct GatedParams {
-  const float* bias;    // [2F], on 16 bytes, or null
+  const float* bias;    // [2F] or null
   const void* dY;       // [T][F]      (backward)
   void* Y;              // [T][F]; backward: P [T][2F]
-  float* part;          // [4 row tiles][2F] partial sums of db, or null
+  float* part;          // [ceil(T / 32)][2F] partial sums of db, or null
   int T, F;
   int hn;               // columns of h per tile: a multiple of 16, at most 128
-  int rts, fts;         // row tiles, column tiles
+  int rts, fts;         // row tiles (of 256 rows in a pair), column tiles
   int ksteps;           // ceil(C / 64)
 };
 
-// y (or dh and dg) of 8 columns of one row, from the accumulators; bh: the h
-// columns' biases in global memory, g's F further (the same address in every
-// lane, so a broadcast out of L1), or null.
+// y (or dh and dg) of 8 columns of one row, from the accumulators and the
+// columns' biases in shared memory (the same address in every lane).
 template <bool BWD, bool BF16>
-__device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t* g, const float* bh, int F,
+__device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t* g, const float* bh, const float* bg,
                                                const uint4& dy, float* o0, float* o1) {
   float d[8];
   if constexpr (BWD) unpack8<BF16>(dy, d);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    float4 bv = make_float4(0.f, 0.f, 0.f, 0.f), gv = bv;
-    if (bh != nullptr) {
-      bv = __ldg(reinterpret_cast<const float4*>(bh) + q);
-      gv = __ldg(reinterpret_cast<const float4*>(bh + F) + q);
-    }
+    const float4 bv = reinterpret_cast<const float4*>(bh)[q], gv = reinterpret_cast<const float4*>(bg)[q];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int e = 4 * q + 2 * k;
@@ -162,30 +223,40 @@ __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t
 }
 
 // Roles: warp 0 TMA (a ring of x / W stages), warp 1 MMA (tcgen05 SS,
-// 128 x 2 hn x 16, two accumulators so that a tile's epilogue overlaps the
-// next tile's products), warps 4..11 epilogue: two warps per quarter of the
-// tile's rows, each taking half of its columns.  Whole tiles (hn = 128) leave
-// through shared memory and TMA stores of 32 rows x 64 columns, which also
-// clip at the edges; narrower ones are stored 16 bytes per thread.
-template <bool BF16, bool BWD, bool FULL>
+// 128 or, in a pair, 256 x 2 hn x 16; two accumulators so that a tile's
+// epilogue overlaps the next tile's products), warp 2 the tiles' biases, warps
+// 4..19 epilogue: four warps per quarter of the CTA's 128 rows, dividing the
+// tile's columns.  (With two warps per quarter the epilogue's dependent chains
+// set the pace: 16 images at 64x64 took 123 us.)
+// PAIR: tiles of 256 rows by 128 columns of h, a CTA of the pair holding the h
+// rows of W's tile and the other the g rows; the results leave through shared
+// memory and TMA stores of 32 rows x 32 columns, which also clip at the edges.
+// Otherwise tiles of 128 rows by hn columns, stored 16 bytes per thread.
+template <bool BF16, bool BWD, bool PAIR>
 __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
     gated_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmY, const GatedParams p) {
   using C = GatedCfg;
-  using S = GatedSmem<BWD>;
+  using S = GatedSmem<BWD, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-  uint64_t* full = bars;                     // [STAGES] TMA -> MMA
+  uint64_t* full = bars;                     // [STAGES] TMA -> MMA (the leader's; both CTAs' loads)
   uint64_t* empty = full + S::STAGES;        // [STAGES] MMA -> TMA
   uint64_t* acc_full = empty + S::STAGES;    // [2] MMA -> epilogue
-  uint64_t* acc_empty = acc_full + 2;        // [2] epilogue -> MMA
-  uint64_t* drain_bar = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + 2;        // [2] epilogue -> MMA (the leader's; both CTAs' warps)
+  uint64_t* bias_full = acc_empty + 2;       // [2] bias warp -> epilogue
+  uint64_t* bias_empty = bias_full + 2;      // [2] back
+  uint64_t* drain_bar = bias_empty + 2;
+  float* sbias = reinterpret_cast<float*>(smem + S::OFF_BIAS);
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);   // [0] tensor memory, [1] abort
   volatile uint32_t* abort_flag = misc + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hn = FULL ? 128 : p.hn;
+  const int hn = PAIR ? 128 : p.hn;
   const int tiles = p.rts * p.fts;
+  const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
+  const int u0 = PAIR ? blockIdx.x / 2 : blockIdx.x, ustep = PAIR ? gridDim.x / 2 : gridDim.x;
+  constexpr int TROWS = PAIR ? 256 : 128;    // rows per tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
@@ -194,7 +265,9 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * C::EPI);
+      mbar_init(&bias_full[i], 1);
+      mbar_init(&bias_empty[i], C::EPI);
     }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
@@ -203,14 +276,19 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
-    if (FULL) tma_prefetch_desc(&tmY);
+    if (PAIR) tma_prefetch_desc(&tmY);
   }
   if (warp == 1) {
-    tmem_alloc(&misc[0], C::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&misc[0], C::TMEM_COLS);
+    } else {
+      tmem_alloc(&misc[0], C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();        // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = misc[0];
   grid_dependency_wait();
@@ -219,35 +297,43 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
     if (lane == 0) {
-      const uint32_t bytes = C::A_BYTES + 2 * hn * 128;
+      const uint32_t bytes = PAIR ? 2 * (C::A_BYTES + 128 * 128) : C::A_BYTES + 2 * hn * 128;
       uint32_t c = 0;
       bool live = true;
-      for (int u = blockIdx.x; u < tiles && live; u += gridDim.x) {
+      for (int u = u0; u < tiles && live; u += ustep) {
         const int rt = u / p.fts, ft = u - rt * p.fts;
         for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
           const uint32_t st = c % S::STAGES, n = c / S::STAGES;
           if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-          uint8_t* s = smem + st * C::STAGE;
-          mbar_arrive_expect_tx(&full[st], bytes);
-          tma_load_3d(s, &tmX, ks * C::BK, rt * 128, 0, &full[st]);
-          tma_load_3d(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, &full[st]);
-          tma_load_3d(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, &full[st]);
+          uint8_t* s = smem + st * S::STAGE;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          if constexpr (PAIR) {
+            const uint32_t bar = cluster_addr(&full[st], 0);
+            tma_load_3d_pair(s, &tmX, ks * C::BK, rt * TROWS + rank * 128, 0, bar);
+            tma_load_3d_pair(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, rank, bar);
+          } else {
+            tma_load_3d(s, &tmX, ks * C::BK, rt * TROWS, 0, &full[st]);
+            tma_load_3d(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, &full[st]);
+            tma_load_3d(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, &full[st]);
+          }
         }
       }
-      // every load this thread issued lands before the CTA can exit
-      volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
-        const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
-        mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
+      // every load lands before the CTA (or its pair) can exit
+      if (rank == 0) {
+        volatile uint32_t never = 0;
+        for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
+          const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
+          mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
+        }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
-    const uint32_t idesc = idesc_f16(128, 2 * hn, BF16, false, false);
+    const uint32_t idesc = idesc_f16(TROWS, 2 * hn, BF16, false, false);
     const uint32_t base = smem_u32(smem);
     uint32_t c = 0, ui = 0;
     bool live = true;
-    for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
+    for (int u = u0; u < tiles && live; u += ustep, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
       if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
       tc_fence_after();
@@ -255,55 +341,100 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         const uint32_t st = c % S::STAGES, n = c / S::STAGES;
         if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
         tc_fence_after();
-        const uint32_t s = base + st * C::STAGE;
+        const uint32_t s = base + st * S::STAGE;
 #pragma unroll
-        for (int kk = 0; kk < C::BK / 16; ++kk)
-          mma_ss(tmem + ab * 256, sdesc_sw128(s + kk * 32, 16, 1024), sdesc_sw128(s + C::A_BYTES + kk * 32, 16, 1024),
-                 idesc, (ks > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[st]);
+        for (int kk = 0; kk < C::BK / 16; ++kk) {
+          const uint64_t ad = sdesc_sw128(s + kk * 32, 16, 1024), bd = sdesc_sw128(s + C::A_BYTES + kk * 32, 16, 1024);
+          const uint32_t acc = (ks > 0 || kk > 0) ? 1u : 0u;
+          if constexpr (PAIR) {
+            mma_ss_pair(tmem + ab * 256, ad, bd, idesc, acc);
+          } else {
+            mma_ss(tmem + ab * 256, ad, bd, idesc, acc);
+          }
+        }
+        if constexpr (PAIR) {
+          mma_commit_pair(&empty[st]);
+        } else {
+          mma_commit(&empty[st]);
+        }
       }
-      if (live) mma_commit(&acc_full[ab]);
+      if (live) {
+        if constexpr (PAIR) {
+          mma_commit_pair(&acc_full[ab]);
+        } else {
+          mma_commit(&acc_full[ab]);
+        }
+      }
     }
     volatile uint32_t never = 0;
-    mma_commit(drain_bar);
+    if constexpr (PAIR) {
+      mma_commit_pair(drain_bar);
+    } else {
+      mma_commit(drain_bar);
+    }
     mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+  } else if (warp == 2) {
+    // ------------------------------ biases ------------------------------------
+    uint32_t ui = 0;
+    for (int u = u0; u < tiles; u += ustep, ++ui) {
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      if (!mbar_wait_warp(&bias_empty[ab], (na & 1) ^ 1, kSiteVEmpty, abort_flag)) break;
+      const int f = (u % p.fts) * hn;
+      for (int j = lane; j < hn; j += 32) {
+        const bool ok = p.bias != nullptr && f + j < p.F;   // columns past F take none: their products are zero
+        sbias[ab * 256 + j] = ok ? __ldg(p.bias + f + j) : 0.f;
+        sbias[ab * 256 + 128 + j] = ok ? __ldg(p.bias + p.F + f + j) : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bias_full[ab]);
+    }
   } else if (warp >= 4) {
     // ------------------------------ epilogue ----------------------------------
-    constexpr int CW = FULL ? 32 : 8;             // columns per pass
-    const int quarter = warp & 3, half = (warp - 4) >> 2, ew = warp - 4;
-    const int hw = hn / 2;                        // columns per warp
+    constexpr int CW = PAIR ? 16 : 8;             // columns per pass
+    const int quarter = warp & 3, part = (warp - 4) >> 2, ew = warp - 4;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stg = smem + S::OFF_STG + ew * S::WSTG;
     uint32_t ui = 0;
     bool live = true;
-    for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
+    for (int u = u0; u < tiles && live; u += ustep, ++ui) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
       const uint32_t ab = ui & 1, na = ui >> 1;
-      const int f0 = ft * hn + half * hw;         // this warp's first column of h
-      const int r0 = rt * 128 + quarter * 32, row = r0 + lane;
+      const int r0 = rt * TROWS + rank * 128 + quarter * 32, row = r0 + lane;
       const bool row_ok = row < p.T;
-      live = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], na & 1, kSiteAccFull, abort_flag));
+      const uint16_t* dy_row = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + ft * hn;
+      uint4 dys[4];
+      if constexpr (BWD && PAIR) {                // dy does not wait for the products
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = part * 32 + q * 8;
+          dys[q] = row_ok && ft * hn + c < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c)) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      live = mbar_wait_warp(&bias_full[ab], na & 1, kSiteVFull, abort_flag) &&
+             mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag);
       if (!live) break;
       tc_fence_after();
-      if constexpr (FULL) {
-        if (lane == 0) bulk_wait_read<0>();   // the staging buffers' previous stores have read them
+      if constexpr (PAIR) {
+        if (lane == 0) bulk_wait_read<0>();       // the staging buffers' previous stores have read them
         __syncwarp();
       }
-#pragma unroll 1
-      for (int c0 = 0; c0 < hw; c0 += CW) {
-        const int f = f0 + c0;
+      // PAIR: this warp's 32 columns in two passes; otherwise every fourth 8 columns
+      const int first = PAIR ? part * 32 : part * 8, step = PAIR ? CW : 32, last = PAIR ? first + 32 : hn;
+#pragma unroll (PAIR ? 2 : 1)
+      for (int c0 = first; c0 < last; c0 += step) {
+        const int f = ft * hn + c0;
         uint4 dy[CW / 8];
-        if constexpr (BWD) {
-          const uint16_t* src = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + f;
-#pragma unroll
-          for (int q = 0; q < CW / 8; ++q)
-            dy[q] = row_ok && f + 8 * q < p.F ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
+        if constexpr (BWD && PAIR) {
+          dy[0] = dys[(c0 - first) / 8];
+          dy[1] = dys[(c0 - first) / 8 + 1];
+        } else if constexpr (BWD) {
+          dy[0] = row_ok && f < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c0)) : make_uint4(0, 0, 0, 0);
         }
         uint32_t h[CW], g[CW];
-        const uint32_t at = tmem + ab * 256 + half * hw + c0 + lane_off;
-        if constexpr (FULL) {
-          tmem_ld_x32(at, h);
-          tmem_ld_x32(at + hn, g);
+        const uint32_t at = tmem + ab * 256 + c0 + lane_off;
+        if constexpr (PAIR) {
+          tmem_ld_x16(at, h);
+          tmem_ld_x16(at + hn, g);
         } else {
           tmem_ld_x8(at, h);
           tmem_ld_x8(at + hn, g);
@@ -311,19 +442,18 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         tmem_wait_ld();
         reg_fence<CW>(h);
         reg_fence<CW>(g);
+        const float* bh = sbias + ab * 256 + c0;
         float o0[CW], o1[CW];
 #pragma unroll
-        for (int q = 0; q < CW / 8; ++q) {
-          // columns past F (their accumulators are zero) take no bias
-          const float* bh = p.bias != nullptr && f + 8 * q < p.F ? p.bias + f + 8 * q : nullptr;
-          gated_columns8<BWD, BF16>(h + 8 * q, g + 8 * q, bh, p.F, dy[q], o0 + 8 * q, o1 + 8 * q);
-        }
-        if constexpr (FULL) {
+        for (int q = 0; q < CW / 8; ++q)
+          gated_columns8<BWD, BF16>(h + 8 * q, g + 8 * q, bh + 8 * q, bh + 128 + 8 * q, dy[q], o0 + 8 * q, o1 + 8 * q);
+        if constexpr (PAIR) {
+          // rows of 64 bytes, 64-byte swizzle: chunk ^ row / 2
 #pragma unroll
           for (int q = 0; q < CW / 8; ++q) {
-            const int ch = ((c0 / 8 + q) ^ (lane & 7)) << 4;
-            *reinterpret_cast<uint4*>(stg + lane * 128 + ch) = pack8<BF16>(o0 + 8 * q);
-            if constexpr (BWD) *reinterpret_cast<uint4*>(stg + 4096 + lane * 128 + ch) = pack8<BF16>(o1 + 8 * q);
+            const int ch = (((c0 - first) / 8 + q) ^ (lane >> 1 & 3)) << 4;
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ch) = pack8<BF16>(o0 + 8 * q);
+            if constexpr (BWD) *reinterpret_cast<uint4*>(stg + 2048 + lane * 64 + ch) = pack8<BF16>(o1 + 8 * q);
           }
         } else if (row_ok && f < p.F) {
           uint16_t* dst = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * (BWD ? 2 * p.F : p.F) + f;
@@ -340,8 +470,8 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
             }
             const float s0 = warp_column_sums<CW>(o0, lane), s1 = warp_column_sums<CW>(o1, lane);
             const int j = lane / (32 / CW);
-            if (lane % (32 / CW) == 0 && f + j < p.F) {
-              float* dst = p.part + static_cast<int64_t>(rt * 4 + quarter) * 2 * p.F + f + j;
+            if (lane % (32 / CW) == 0 && f + j < p.F && r0 < p.T) {
+              float* dst = p.part + static_cast<int64_t>(r0 / 32) * 2 * p.F + f + j;
               dst[0] = s0;
               dst[p.F] = s1;
             }
@@ -349,28 +479,38 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         }
       }
       tc_fence_before();
-      if constexpr (FULL) fence_proxy_async_smem();
+      if constexpr (PAIR) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&acc_empty[ab]);
-        if constexpr (FULL) {
+        mbar_arrive(&bias_empty[ab]);
+        if constexpr (PAIR) {
+          mbar_arrive_cluster(cluster_addr(&acc_empty[ab], 0));
+        } else {
+          mbar_arrive(&acc_empty[ab]);
+        }
+        if constexpr (PAIR) {
           // stores start inside the tensor; what runs over its edges is clipped
-          if (f0 < p.F && r0 < p.T) {
-            tma_store_3d(&tmY, stg, f0, r0, 0);
-            if constexpr (BWD) tma_store_3d(&tmY, stg + 4096, f0, r0, 1);
+          if (ft * hn + first < p.F && r0 < p.T) {
+            tma_store_3d(&tmY, stg, ft * hn + first, r0, 0);
+            if constexpr (BWD) tma_store_3d(&tmY, stg + 2048, ft * hn + first, r0, 1);
             bulk_commit();
           }
         }
       }
     }
-    if (FULL && lane == 0) bulk_wait<0>();
+    if (PAIR && lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();        // neither CTA leaves while the other's products read its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    if constexpr (PAIR) {
+      tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    } else {
+      tmem_dealloc(tmem, C::TMEM_COLS);
+    }
   }
 }
 

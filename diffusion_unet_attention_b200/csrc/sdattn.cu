@@ -63,9 +63,11 @@ EncodeTiledFn encode_fn() {
 }
 
 // 3-D tiled map: dims {d0 (contiguous), d1, d2}, byte strides of d1 and d2,
-// box {b0, b1, 1}, 128-byte swizzle, zero fill outside the tensor.
+// box {b0, b1, 1}, 128-byte swizzle unless told otherwise, zero fill outside
+// the tensor.
 bool make_map_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64_t d0, uint64_t d1, uint64_t d2,
-                 uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1) {
+                 uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
@@ -73,7 +75,7 @@ bool make_map_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64
   const cuuint32_t box[3] = {b0, b1, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -231,7 +231,8 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 128)) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, F, 2, C * 2, F * C * 2, 64, static_cast<uint32_t>(p.hn))) return SDATTN_ERR_CUDA;
   const uint64_t ldy = BWD ? 4 * F : 2 * F;   // bytes of a row of y, or of P = [dh, dg]
-  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, BWD ? 32 : 64, 32,
+                   BWD ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return SDATTN_ERR_CUDA;
   const int64_t tiles = int64_t(p.rts) * p.fts;
   if (plan.pair) {

@@ -155,15 +155,15 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 struct GatedCfg {
   static constexpr int BK = 64;                     // columns of C per stage
   static constexpr int A_BYTES = 128 * 128;         // 128 rows of x
   static constexpr int HN = 128;                    // most columns of h (and of g) per tile
-  static constexpr int EPI = 16;                    // epilogue warps
-  static constexpr int NTHREADS = (4 + EPI) * 32;   // TMA, MMA, bias, one idle warp, epilogue
+  static constexpr int EPI = 8;                     // epilogue warps of a tile
+  static constexpr int NTHREADS = (4 + 2 * EPI) * 32;   // TMA, MMA, bias, one idle warp, two groups of epilogue warps
   static constexpr uint32_t TMEM_COLS = 512;        // two accumulators of 2 HN columns
 };
 
@@ -171,11 +171,11 @@ struct GatedCfg {
 template <bool BWD, bool PAIR>
 struct GatedSmem {
   static constexpr int STAGE = GatedCfg::A_BYTES + (PAIR ? 1 : 2) * GatedCfg::HN * 128;
-  static constexpr int STAGES = PAIR && !BWD ? 5 : 4;
-  // an epilogue warp's staged output (PAIR): 32 rows x 32 columns of y, or of dh and of dg
-  static constexpr int WSTG = PAIR ? (BWD ? 4096 : 2048) : 0;
+  static constexpr int STAGES = 4;
+  // an epilogue warp's staged output (PAIR): 32 rows x 64 columns of y, or x 32 of dh and of dg
+  static constexpr int WSTG = PAIR ? 4096 : 0;
   static constexpr int OFF_STG = STAGES * STAGE;
-  static constexpr int OFF_BIAS = OFF_STG + GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
+  static constexpr int OFF_BIAS = OFF_STG + 2 * GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
   static constexpr int OFF_BAR = OFF_BIAS + 2 * 2 * GatedCfg::HN * 4;
   static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;
   static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;
@@ -225,12 +225,14 @@ __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t
 // Roles: warp 0 TMA (a ring of x / W stages), warp 1 MMA (tcgen05 SS,
 // 128 or, in a pair, 256 x 2 hn x 16; two accumulators so that a tile's
 // epilogue overlaps the next tile's products), warp 2 the tiles' biases, warps
-// 4..19 epilogue: four warps per quarter of the CTA's 128 rows, dividing the
-// tile's columns.  (With two warps per quarter the epilogue's dependent chains
-// set the pace: 16 images at 64x64 took 123 us.)
+// 4..19 epilogue: two groups of eight on alternate tiles, so that one group's
+// waits and hand-offs pass under the other's arithmetic; in a group two warps
+// per quarter of the CTA's 128 rows, dividing the tile's columns.  (16 images
+// at 64x64: one group of eight warps 123 us, one of sixteen 117 us.)
 // PAIR: tiles of 256 rows by 128 columns of h, a CTA of the pair holding the h
 // rows of W's tile and the other the g rows; the results leave through shared
-// memory and TMA stores of 32 rows x 32 columns, which also clip at the edges.
+// memory and TMA stores of 32 rows x 64 columns of y, or 32 of dh and of dg,
+// which also clip at the edges.
 // Otherwise tiles of 128 rows by hn columns, stored 16 bytes per thread.
 template <bool BF16, bool BWD, bool PAIR>
 __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
@@ -391,44 +393,30 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   } else if (warp >= 4) {
     // ------------------------------ epilogue ----------------------------------
     constexpr int CW = PAIR ? 16 : 8;             // columns per pass
-    const int quarter = warp & 3, part = (warp - 4) >> 2, ew = warp - 4;
+    const int quarter = warp & 3, part = (warp - 4) >> 2 & 1, grp = (warp - 4) >> 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stg = smem + S::OFF_STG + ew * S::WSTG;
-    uint32_t ui = 0;
-    bool live = true;
-    for (int u = u0; u < tiles && live; u += ustep, ++ui) {
+    uint8_t* stg = smem + S::OFF_STG + (warp - 4) * S::WSTG;
+    uint32_t na = 0;                              // tiles of this group
+    for (int u = u0 + grp * ustep; u < tiles; u += 2 * ustep, ++na) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
-      const uint32_t ab = ui & 1, na = ui >> 1;
+      const uint32_t ab = grp;
       const int r0 = rt * TROWS + rank * 128 + quarter * 32, row = r0 + lane;
       const bool row_ok = row < p.T;
       const uint16_t* dy_row = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + ft * hn;
-      uint4 dys[4];
-      if constexpr (BWD && PAIR) {                // dy does not wait for the products
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = part * 32 + q * 8;
-          dys[q] = row_ok && ft * hn + c < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c)) : make_uint4(0, 0, 0, 0);
-        }
-      }
-      live = mbar_wait_warp(&bias_full[ab], na & 1, kSiteVFull, abort_flag) &&
-             mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag);
-      if (!live) break;
+      if (!mbar_wait_warp(&bias_full[ab], na & 1, kSiteVFull, abort_flag) ||
+          !mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag))
+        break;
       tc_fence_after();
-      if constexpr (PAIR) {
-        if (lane == 0) bulk_wait_read<0>();       // the staging buffers' previous stores have read them
-        __syncwarp();
-      }
-      // PAIR: this warp's 32 columns in two passes; otherwise every fourth 8 columns
-      const int first = PAIR ? part * 32 : part * 8, step = PAIR ? CW : 32, last = PAIR ? first + 32 : hn;
-#pragma unroll (PAIR ? 2 : 1)
+      // PAIR: this warp's 64 columns; otherwise every other 8 columns
+      const int first = PAIR ? part * 64 : part * 8, step = PAIR ? CW : 16, last = PAIR ? first + 64 : hn;
+#pragma unroll 1
       for (int c0 = first; c0 < last; c0 += step) {
         const int f = ft * hn + c0;
         uint4 dy[CW / 8];
-        if constexpr (BWD && PAIR) {
-          dy[0] = dys[(c0 - first) / 8];
-          dy[1] = dys[(c0 - first) / 8 + 1];
-        } else if constexpr (BWD) {
-          dy[0] = row_ok && f < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c0)) : make_uint4(0, 0, 0, 0);
+        if constexpr (BWD) {
+#pragma unroll
+          for (int q = 0; q < CW / 8; ++q)
+            dy[q] = row_ok && f + 8 * q < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c0) + q) : make_uint4(0, 0, 0, 0);
         }
         uint32_t h[CW], g[CW];
         const uint32_t at = tmem + ab * 256 + c0 + lane_off;
@@ -448,12 +436,33 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         for (int q = 0; q < CW / 8; ++q)
           gated_columns8<BWD, BF16>(h + 8 * q, g + 8 * q, bh + 8 * q, bh + 128 + 8 * q, dy[q], o0 + 8 * q, o1 + 8 * q);
         if constexpr (PAIR) {
-          // rows of 64 bytes, 64-byte swizzle: chunk ^ row / 2
+          if (BWD ? (c0 & 31) == 0 : c0 == first) {
+            if (lane == 0) bulk_wait_read<0>();   // the buffer's previous stores have read it
+            __syncwarp();
+          }
 #pragma unroll
           for (int q = 0; q < CW / 8; ++q) {
-            const int ch = (((c0 - first) / 8 + q) ^ (lane >> 1 & 3)) << 4;
-            *reinterpret_cast<uint4*>(stg + lane * 64 + ch) = pack8<BF16>(o0 + 8 * q);
-            if constexpr (BWD) *reinterpret_cast<uint4*>(stg + 2048 + lane * 64 + ch) = pack8<BF16>(o1 + 8 * q);
+            if constexpr (BWD) {
+              // rows of 64 bytes, 64-byte swizzle: chunk ^ row / 2
+              const int ch = (((c0 & 31) / 8 + q) ^ (lane >> 1 & 3)) << 4;
+              *reinterpret_cast<uint4*>(stg + lane * 64 + ch) = pack8<BF16>(o0 + 8 * q);
+              *reinterpret_cast<uint4*>(stg + 2048 + lane * 64 + ch) = pack8<BF16>(o1 + 8 * q);
+            } else {
+              // rows of 128 bytes, 128-byte swizzle: chunk ^ row
+              const int ch = (((c0 & 63) / 8 + q) ^ (lane & 7)) << 4;
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ch) = pack8<BF16>(o0 + 8 * q);
+            }
+          }
+          if (BWD ? (c0 & 31) == 16 : c0 + CW == last) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            // stores start inside the tensor; what runs over its edges is clipped
+            const int fs = ft * hn + (BWD ? c0 - 16 : first);
+            if (lane == 0 && fs < p.F && r0 < p.T) {
+              tma_store_3d(&tmY, stg, fs, r0, 0);
+              if constexpr (BWD) tma_store_3d(&tmY, stg + 2048, fs, r0, 1);
+              bulk_commit();
+            }
           }
         } else if (row_ok && f < p.F) {
           uint16_t* dst = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * (BWD ? 2 * p.F : p.F) + f;
@@ -479,7 +488,6 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         }
       }
       tc_fence_before();
-      if constexpr (PAIR) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bias_empty[ab]);
@@ -487,14 +495,6 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
           mbar_arrive_cluster(cluster_addr(&acc_empty[ab], 0));
         } else {
           mbar_arrive(&acc_empty[ab]);
-        }
-        if constexpr (PAIR) {
-          // stores start inside the tensor; what runs over its edges is clipped
-          if (ft * hn + first < p.F && r0 < p.T) {
-            tma_store_3d(&tmY, stg, ft * hn + first, r0, 0);
-            if constexpr (BWD) tma_store_3d(&tmY, stg + 2048, ft * hn + first, r0, 1);
-            bulk_commit();
-          }
         }
       }
     }

@@ -639,9 +639,11 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
     b = _vector(bias, K, x.device, "bias")
     x, w = _contig(x), _contig(w)
     y = _out(out, x, x.shape[:-1] + (K,))
-    _call(x.device, _lib_handle().sdattn_adapter_linear,
-          _shape(_lib.AdapterDesc, T, C, K, L, R, rows, _DTYPES[x.dtype]), x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(down),
-          _ptr(up), _ptr(scale), _ptr(ids), y.data_ptr())
+    fields = (T, C, K, L, R, rows, _DTYPES[x.dtype])
+    need = _bytes(x.device, "sdattn_adapter_linear_workspace_bytes", _lib.AdapterDesc, *fields) if L else 0
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    _call(x.device, _lib_handle().sdattn_adapter_linear, _shape(_lib.AdapterDesc, *fields), x.data_ptr(), w.data_ptr(),
+          _ptr(b), _ptr(down), _ptr(up), _ptr(scale), _ptr(ids), y.data_ptr(), _ptr(ws), need)
     return y
 
 

@@ -34,7 +34,7 @@ EXPORTS = ("sdattn_a_ld", "sdattn_workspace_bytes", "sdattn_qk_stats", "sdattn_s
            "sdattn_wino_filter_bytes", "sdattn_wino_workspace_bytes", "sdattn_wino_filter", "sdattn_wino_conv3x3",
            "sdattn_layer_norm", "sdattn_layer_norm_bwd_workspace_bytes", "sdattn_layer_norm_bwd",
            "sdattn_gated_ff", "sdattn_gated_ff_bwd_workspace_bytes", "sdattn_gated_ff_bwd",
-           "sdattn_adapter_linear",
+           "sdattn_adapter_linear_workspace_bytes", "sdattn_adapter_linear",
            "sdattn_device_error", "sdattn_status_string", "sdattn_version")
 
 
@@ -145,7 +145,9 @@ def load(path: str = LIB_PATH):
     lib.sdattn_gated_ff_bwd_workspace_bytes.restype = sz
     lib.sdattn_gated_ff_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdattn_gated_ff_bwd.restype = ctypes.c_int
-    lib.sdattn_adapter_linear.argtypes = [ctypes.POINTER(AdapterDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sdattn_adapter_linear_workspace_bytes.argtypes = [ctypes.POINTER(AdapterDesc)]
+    lib.sdattn_adapter_linear_workspace_bytes.restype = sz
+    lib.sdattn_adapter_linear.argtypes = [ctypes.POINTER(AdapterDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdattn_adapter_linear.restype = ctypes.c_int
     lib.sdattn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.sdattn_device_error.restype = ctypes.c_int

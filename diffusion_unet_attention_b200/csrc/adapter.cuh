@@ -21,9 +21,15 @@
 // tile's distinct adapters; each contributes ceil(R / 64) slots of rc ranks
 // (R rounded up to 16, at most 64), and 64 / rc slots fit a phase.  Phase 0
 // runs with x W^T; a tile of more slots runs through x again, once per phase,
-// against D alone.  The MMA warp issues the next phase's (or tile's) x
-// products before it waits for the conversion of the last one's z, so the
-// conversion is hidden except at the end.
+// against D alone.  The MMA warp starts the next phase's (or tile's) x
+// products and adds the last one's z U^T half way through them, so that the
+// conversion of z passes under products.
+//
+// Few rows with an adapter each (the time embedding's projection, single
+// tokens) would cost a phase for every few rows.  There the adapters are
+// per-row work, bound by reading D and U once for each row: adapter_z_kernel
+// computes z with plain fp32 sums (a warp per row and two ranks), and the
+// projection's epilogue adds z U^T, 8 ranks of 32 columns at a time (ROWS).
 #pragma once
 
 #include "unet_ops.cuh"
@@ -32,17 +38,16 @@ namespace sdattn {
 
 struct AdapterCfg {
   static constexpr int BK = 64;
-  static constexpr int X_BYTES = 128 * 128;
   static constexpr int BN = 192;                    // most columns per tile
-  static constexpr int W_BYTES = BN * 128;
   static constexpr int ZN = 64;                     // ranks per phase
-  static constexpr int D_BYTES = ZN * 128;
-  static constexpr int STAGE = X_BYTES + W_BYTES + D_BYTES;
-  static constexpr int STAGES = 4;
-  static constexpr int OFF_PLAN = STAGES * STAGE;
-  static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' adapters, rows' scales, count
-  static constexpr int OFF_BAR = OFF_PLAN + 2 * PLAN;
-  static constexpr int NBAR = 2 * STAGES + 4 + 4 + 4 + 1;
+  static constexpr int RING = 217088;               // bytes of the ring of stages
+  static constexpr int SLACK = 16384;               // kept behind it when x's tiles are short: their products read up to 16 KB past a stage
+  static constexpr int MAX_STAGES = 20;
+  static constexpr int OFF_PLAN = RING;
+  static constexpr int PLANS = 4;                   // tiles the planner may run ahead
+  static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' places, rows' scales, count
+  static constexpr int OFF_BAR = OFF_PLAN + PLANS * PLAN;
+  static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 2 * PLANS + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static constexpr int NTHREADS = 384;              // TMA, MMA, planner, idle, eight epilogue warps
   static constexpr uint32_t TMEM_COLS = 512;
@@ -54,15 +59,58 @@ struct AdapterParams {
   const float* bias;      // [K], on 16 bytes, or null
   const int32_t* ids;     // [T / rows], or null: no adapters
   const float* scale;     // [L], or null: ones
+  const float* z;         // ROWS: [T][R], scaled
+  const void* U;          // ROWS: [L][K][R]
   void* Y;                // [T][K]
-  int T, K, L, rows;      // rows: rows per id
+  int T, K, L, R, rows;   // rows: rows per id
   int bn;                 // columns per tile: a multiple of 16 up to 192
-  int tm;                 // rows per tile, up to 128
+  int tm;                 // rows per tile: 128, or all rows of a shorter x rounded up to 8
   int rts, nts;           // row tiles, column tiles
   int ksteps;             // ceil(C / 64)
   int rc;                 // ranks per slot: 16, 32, 48 or 64
   int chunks;             // slots per adapter: ceil(R / 64)
+  int stages, stage;      // of the ring: how many, bytes of one (x, then W or U, then D)
 };
+
+// z[t][r] = s_i x[t] . D_i[r], one warp per row and pair of ranks.
+template <bool BF16>
+__global__ void __launch_bounds__(256) adapter_z_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ D,
+                                                        const float* __restrict__ scale, const int32_t* __restrict__ ids,
+                                                        float* __restrict__ z, int T, int C, int L, int R, int rows) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int t = static_cast<int>(w / (R / 2)), r = static_cast<int>(w - static_cast<int64_t>(t) * (R / 2)) * 2;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (t >= T) return;
+  const int id = __ldg(ids + t / rows);
+  if (id < 0 || id >= L) return;                    // nobody reads this row of z
+  const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(t) * C);
+  const uint4* d0 = reinterpret_cast<const uint4*>(D + (static_cast<int64_t>(id) * R + r) * C);
+  const uint4* d1 = reinterpret_cast<const uint4*>(D + (static_cast<int64_t>(id) * R + r + 1) * C);
+  float a = 0.f, b = 0.f;
+#pragma unroll 5
+  for (int i = lane; i < C / 8; i += 32) {
+    float fx[8], f0[8], f1[8];
+    unpack8<BF16>(__ldg(x + i), fx);
+    unpack8<BF16>(__ldg(d0 + i), f0);
+    unpack8<BF16>(__ldg(d1 + i), f1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a = fmaf(fx[e], f0[e], a);
+      b = fmaf(fx[e], f1[e], b);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, off);
+    b += __shfl_xor_sync(0xffffffffu, b, off);
+  }
+  if (lane == 0) {
+    const float s = scale != nullptr ? __ldg(scale + id) : 1.f;
+    *reinterpret_cast<float2*>(z + static_cast<int64_t>(t) * R + r) = make_float2(a * s, b * s);
+  }
+}
 
 // One tile's plan in shared memory.
 struct AdapterPlan {
@@ -74,7 +122,7 @@ struct AdapterPlan {
 };
 static_assert(sizeof(AdapterPlan) == AdapterCfg::PLAN, "plan layout");
 
-template <bool BF16>
+template <bool BF16, bool ROWS>
 __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     adapter_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
@@ -83,24 +131,28 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* full = bars;                      // [STAGES] TMA -> MMA
-  uint64_t* empty = full + C::STAGES;         // [STAGES] MMA -> TMA
-  uint64_t* acc_full = empty + C::STAGES;     // [2] MMA -> epilogue
+  uint64_t* full = bars;                      // [stages] TMA -> MMA
+  uint64_t* empty = full + C::MAX_STAGES;     // [stages] MMA -> TMA
+  uint64_t* acc_full = empty + C::MAX_STAGES; // [2] MMA -> epilogue
   uint64_t* acc_empty = acc_full + 2;         // [2] epilogue -> MMA
   uint64_t* z_full = acc_empty + 2;           // [2] MMA -> epilogue: z is complete
   uint64_t* p_full = z_full + 2;              // [2] epilogue -> MMA: z is converted
-  uint64_t* plan_full = p_full + 2;           // [2] planner -> TMA, MMA, epilogue
-  uint64_t* plan_empty = plan_full + 2;       // [2] back
-  uint64_t* drain_bar = plan_empty + 2;
+  uint64_t* plan_full = p_full + 2;           // [PLANS] planner -> TMA, MMA, epilogue
+  uint64_t* plan_empty = plan_full + C::PLANS;   // [PLANS] back
+  uint64_t* drain_bar = plan_empty + C::PLANS;
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile uint32_t* abort_flag = misc + 1;
   AdapterPlan* plans = reinterpret_cast<AdapterPlan*>(smem + C::OFF_PLAN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = p.rts * p.nts;
   const int spp = C::ZN / p.rc;               // slots per phase
+  const bool planned = !ROWS && p.ids != nullptr;
+  const uint32_t NS = p.stages;
+  const int off_w = p.tm * 128, off_d = off_w + p.bn * 128;
+  const int mid = p.ksteps / 2;               // the step of x's products after which the last phase's z U^T goes
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -109,6 +161,8 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       mbar_init(&acc_empty[i], 8);
       mbar_init(&z_full[i], 1);
       mbar_init(&p_full[i], 8);
+    }
+    for (int i = 0; i < C::PLANS; ++i) {
       mbar_init(&plan_full[i], 1);
       mbar_init(&plan_empty[i], 10);
     }
@@ -119,7 +173,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
-    if (p.ids != nullptr) {
+    if (planned) {
       tma_prefetch_desc(&tmD);
       tma_prefetch_desc(&tmU);
     }
@@ -142,8 +196,8 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   if (warp == 2) {
     // ------------------------------ planner -----------------------------------
     uint32_t ui = 0;
-    for (int u = blockIdx.x; u < tiles; u += gridDim.x, ++ui) {
-      const uint32_t pb = ui & 1, n = ui >> 1;
+    for (int u = blockIdx.x; planned && u < tiles; u += gridDim.x, ++ui) {
+      const uint32_t pb = ui % C::PLANS, n = ui / C::PLANS;
       if (!mbar_wait_warp(&plan_empty[pb], (n & 1) ^ 1, kSiteTicket, abort_flag)) break;
       AdapterPlan* pl = &plans[pb];
       const int r0 = u / p.nts * p.tm;
@@ -152,7 +206,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       for (int q = 0; q < 4; ++q) {
         const int r = lane + 32 * q;
         id[q] = -1;
-        if (p.ids != nullptr && r < p.tm && r0 + r < p.T) {
+        if (r < p.tm && r0 + r < p.T) {
           const int v = __ldg(p.ids + (r0 + r) / p.rows);
           if (v >= 0 && v < p.L) id[q] = v;
         }
@@ -194,53 +248,58 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const int ns = slots_of(pl->count, pend_ph);
         for (int j = 0; j < ns && live; ++j, ++c) {
           const int s = pend_ph * spp + j, a = pl->adapter[s / p.chunks], ch = s % p.chunks;
-          const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+          const uint32_t st = c % NS, n = c / NS;
           if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
           mbar_arrive_expect_tx(&full[st], p.bn * 128);
-          tma_load_3d(smem + st * C::STAGE + C::X_BYTES, &tmU, ch * 64, pend_n0, a, &full[st]);
+          tma_load_3d(smem + st * p.stage + off_w, &tmU, ch * 64, pend_n0, a, &full[st]);
         }
         if (pend_last) mbar_arrive(&plan_empty[pend_pb]);
         pend = false;
       };
       for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
         const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
-        const uint32_t pb = ui & 1;
-        if (!mbar_wait(&plan_full[pb], (ui >> 1) & 1, kSiteTicket, abort_flag)) { live = false; break; }
+        const uint32_t pb = ui % C::PLANS;
+        if (planned && !mbar_wait(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag)) { live = false; break; }
         const AdapterPlan* pl = &plans[pb];
-        const int count = pl->count, nph = phases(count);
+        const int count = planned ? pl->count : 0, nph = phases(count);
         for (int ph = 0; ph < nph && live; ++ph) {
           const int ns = slots_of(count, ph);
           const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + max(ns, 0) * p.rc * 128;
           for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-            const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+            const uint32_t st = c % NS, n = c / NS;
             if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-            uint8_t* s = smem + st * C::STAGE;
+            uint8_t* s = smem + st * p.stage;
             mbar_arrive_expect_tx(&full[st], bytes);
             tma_load_3d(s, &tmX, ks * C::BK, rt * p.tm, 0, &full[st]);
-            if (ph == 0) tma_load_3d(s + C::X_BYTES, &tmW, ks * C::BK, n0, 0, &full[st]);
+            if (ph == 0) tma_load_3d(s + off_w, &tmW, ks * C::BK, n0, 0, &full[st]);
             for (int j = 0; j < ns; ++j) {
               const int sl = ph * spp + j;
-              tma_load_3d(s + C::X_BYTES + C::W_BYTES + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
+              tma_load_3d(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
                           pl->adapter[sl / p.chunks], &full[st]);
             }
+            if (ks == mid && pend) {
+              ++c;                              // this step's stage
+              load_up();
+              if (!live) break;
+              --c;                              // counted by the loop
+            }
           }
-          if (pend && live) load_up();
           if (ns > 0) {
             pend = true;
             pend_ph = ph;
             pend_n0 = n0;
             pend_pb = pb;
             pend_last = ph == nph - 1;
-          } else {
-            mbar_arrive(&plan_empty[pb]);   // a tile without adapters
+          } else if (planned) {
+            mbar_arrive(&plan_empty[pb]);       // a tile without adapters
           }
         }
       }
       if (pend && live) load_up();
       // every load this thread issued lands before the CTA can exit
       volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < C::STAGES && st < c; ++st) {
-        const uint32_t uses = (c - st + C::STAGES - 1) / C::STAGES;
+      for (uint32_t st = 0; st < NS && st < c; ++st) {
+        const uint32_t uses = (c - st + NS - 1) / NS;
         mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
       }
     }
@@ -260,10 +319,10 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       tc_fence_after();
       const int ns = slots_of(pend_count, pend_ph);
       for (int j = 0; j < ns; ++j, ++c) {
-        const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+        const uint32_t st = c % NS, n = c / NS;
         if (!mbar_wait_warp(&full[st], n & 1, kSiteVFull, abort_flag)) { live = false; return; }
         tc_fence_after();
-        const uint32_t su = base + st * C::STAGE + C::X_BYTES;
+        const uint32_t su = base + st * p.stage + off_w;
         for (int kk = 0; kk < p.rc / 16; ++kk) {
           const int r = j * p.rc + kk * 16;     // rank within the phase: two per tensor-memory column
           mma_ts(tmem + pend_ab * C::BN, tmem + C::TM_Z + zb * C::ZN + r / 32 * 32 + r % 32 / 2,
@@ -279,8 +338,9 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     };
     for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
-      if (!mbar_wait_warp(&plan_full[ab], na & 1, kSiteTicket, abort_flag)) { live = false; break; }
-      const int count = plans[ab].count, nph = phases(count);
+      const uint32_t pb = ui % C::PLANS;
+      if (planned && !mbar_wait_warp(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag)) { live = false; break; }
+      const int count = planned ? plans[pb].count : 0, nph = phases(count);
       if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
       tc_fence_after();
       for (int ph = 0; ph < nph && live; ++ph) {
@@ -288,34 +348,39 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const uint32_t zb = zc & 1;
         const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
         for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-          const uint32_t st = c % C::STAGES, n = c / C::STAGES;
+          const uint32_t st = c % NS, n = c / NS;
           if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
           tc_fence_after();
-          const uint32_t s = base + st * C::STAGE;
+          const uint32_t s = base + st * p.stage;
 #pragma unroll
           for (int kk = 0; kk < C::BK / 16; ++kk) {
             const uint64_t xd = sdesc_sw128(s + kk * 32, 16, 1024);
             const uint32_t acc = (ks > 0 || kk > 0) ? 1u : 0u;
-            if (ph == 0) mma_ss(tmem + ab * C::BN, xd, sdesc_sw128(s + C::X_BYTES + kk * 32, 16, 1024), idesc_w, acc);
+            if (ph == 0) mma_ss(tmem + ab * C::BN, xd, sdesc_sw128(s + off_w + kk * 32, 16, 1024), idesc_w, acc);
             if (ns > 0)
-              mma_ss(tmem + C::TM_Z + zb * C::ZN, xd, sdesc_sw128(s + C::X_BYTES + C::W_BYTES + kk * 32, 16, 1024),
+              mma_ss(tmem + C::TM_Z + zb * C::ZN, xd, sdesc_sw128(s + off_d + kk * 32, 16, 1024),
                      idesc_d, acc);
           }
           mma_commit(&empty[st]);
+          if (ks == mid && pend) {
+            ++c;
+            mma_up();
+            if (!live) break;
+            --c;
+          }
         }
         if (!live) break;
         if (ns > 0) {
           mma_commit(&z_full[zb]);
         } else {
           mma_commit(&acc_full[ab]);
-          if (lane == 0) mbar_arrive(&plan_empty[ab]);
+          if (planned && lane == 0) mbar_arrive(&plan_empty[pb]);
         }
-        if (pend) mma_up();
         if (ns > 0) {
           pend = true;
           pend_ph = ph;
           pend_count = count;
-          pend_pb = ab;
+          pend_pb = pb;
           pend_ab = ab;
           pend_z = zc++;
           pend_last = ph == nph - 1;
@@ -336,13 +401,24 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       const uint32_t ab = ui & 1, na = ui >> 1;
       const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
       const int r = quarter * 32 + lane, row = rt * p.tm + r;
-      live = mbar_wait_warp(&plan_full[ab], na & 1, kSiteTicket, abort_flag);
-      if (!live) break;
-      const AdapterPlan* pl = &plans[ab];
-      const int count = pl->count, place = pl->place[r];
-      const float scale = pl->scale[r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&plan_empty[ab]);
+      int count = 0, place = -1;
+      float scale = 0.f;
+      if (planned) {
+        const uint32_t pb = ui % C::PLANS;
+        live = mbar_wait_warp(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+        if (!live) break;
+        const AdapterPlan* pl = &plans[pb];
+        count = pl->count;
+        place = pl->place[r];
+        scale = pl->scale[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&plan_empty[pb]);
+      }
+      int id = -1;                              // ROWS: this row's adapter
+      if (ROWS && r < p.tm && row < p.T) {
+        id = __ldg(p.ids + row / p.rows);
+        if (id >= p.L) id = -1;
+      }
       if (count > 0) {
         const int nph = phases(count);
         for (int ph = 0; ph < nph; ++ph, ++zc) {
@@ -377,31 +453,60 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       live = mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag);
       if (!live) break;
       tc_fence_after();
-      // 16 columns at a time, the two warps of a quarter in turn
+      // 32 columns at a time (the last ones 16), the two warps of a quarter in turn
 #pragma unroll 1
-      for (int c0 = half * 16; c0 < p.bn && n0 + c0 < p.K; c0 += 32) {
-        uint32_t v[16];
-        tmem_ld_x16(tmem + ab * C::BN + c0 + lane_off, v);
+      for (int c0 = half * 32; c0 < p.bn && n0 + c0 < p.K; c0 += 64) {
+        uint32_t v[32];
+        tmem_ld_x32(tmem + ab * C::BN + c0 + lane_off, v);
         tmem_wait_ld();
-        reg_fence<16>(v);
-        if (r < p.tm && row < p.T) {
-          uint16_t* dst = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * p.K + n0 + c0;
+        reg_fence<32>(v);
+        if (r >= p.tm || row >= p.T) continue;
+        const int cols = min(min(p.bn - c0, 32), p.K - n0 - c0);   // a multiple of 8
+        float f[32];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (n0 + c0 + 8 * q >= p.K) break;
-            float f[8];
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        if constexpr (ROWS) {
+          if (id >= 0) {
+            const float4* zr = reinterpret_cast<const float4*>(p.z + static_cast<int64_t>(row) * p.R);
+            const uint16_t* up = static_cast<const uint16_t*>(p.U) + (static_cast<int64_t>(id) * p.K + n0 + c0) * p.R;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
-            if (p.bias != nullptr) {
-              const float4* bs = reinterpret_cast<const float4*>(p.bias + n0 + c0 + 8 * q);
-              const float4 b0 = __ldg(bs), b1 = __ldg(bs + 1);
-              f[0] += b0.x; f[1] += b0.y; f[2] += b0.z; f[3] += b0.w;
-              f[4] += b1.x; f[5] += b1.y; f[6] += b1.z; f[7] += b1.w;
+            for (int h = 0; h < 32; h += 16) {    // 16 loads of U in flight
+              for (int r8 = 0; r8 < p.R && h < cols; r8 += 8) {
+                const float4 z0 = __ldg(zr + r8 / 4), z1 = __ldg(zr + r8 / 4 + 1);
+                const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+                for (int j = h; j < h + 16; ++j) {
+                  if (j < cols) {
+                    float w[8];
+                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(up + static_cast<int64_t>(j) * p.R + r8)), w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[j] = fmaf(zz[e], w[e], f[j]);
+                  }
+                }
+              }
             }
-            reinterpret_cast<uint4*>(dst)[q] = pack8<BF16>(f);
           }
         }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * p.K + n0 + c0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q >= cols) break;
+          if (p.bias != nullptr) {
+            const float4* bs = reinterpret_cast<const float4*>(p.bias + n0 + c0 + 8 * q);
+            const float4 b0 = __ldg(bs), b1 = __ldg(bs + 1);
+            f[8 * q] += b0.x;
+            f[8 * q + 1] += b0.y;
+            f[8 * q + 2] += b0.z;
+            f[8 * q + 3] += b0.w;
+            f[8 * q + 4] += b1.x;
+            f[8 * q + 5] += b1.y;
+            f[8 * q + 6] += b1.z;
+            f[8 * q + 7] += b1.w;
+          }
+          dst[q] = pack8<BF16>(f + 8 * q);
+        }
       }
+      __syncwarp();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);

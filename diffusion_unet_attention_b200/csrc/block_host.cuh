@@ -88,7 +88,7 @@ sdattn_status launch_ln_u(const sdattn::LNParams& p, const LNPlan& pl, bool back
   const int g = static_cast<int>(grid);
   bool ok = false;
   if (!pl.cta) {
-    ok = backward ? launch(sdattn::layer_norm_bwd_kernel<DT, VEC, U, false>, g, pl.threads, 2 * p.C * 4, s, p)
+    ok = backward ? launch(sdattn::layer_norm_bwd_kernel<DT, VEC, U, false>, g, pl.threads, pl.threads / 32 * p.C * 4, s, p)
                   : launch(sdattn::layer_norm_kernel<DT, VEC, U, false>, g, pl.threads, 0, s, p);
   } else if constexpr (ln_cta_u(DT, VEC, U)) {
     ok = backward ? launch(sdattn::layer_norm_bwd_kernel<DT, VEC, U, true>, g, pl.threads, 0, s, p)
@@ -144,12 +144,12 @@ bool ln_vec(const sdattn_ln_desc* d, std::initializer_list<const void*> ps) {
 }
 
 // CTAs of the backward pass: two per SM (four when a row takes a small CTA),
-// but at least four rows for each lane group, since every CTA costs a partial
+// but at least two rows for each lane group, since every CTA costs a partial
 // row of sums that the second kernel reads.
 int64_t ln_bwd_grid(const sdattn_ln_desc* d, const LNPlan& pl, int nsm) {
   const int64_t rpc = pl.cta ? 1 : pl.threads / pl.L;
   const int64_t per_sm = pl.cta && pl.threads <= 256 ? 4 : 2;
-  return std::min((d->T + 4 * rpc - 1) / (4 * rpc), static_cast<int64_t>(nsm) * per_sm);
+  return std::min((d->T + 2 * rpc - 1) / (2 * rpc), static_cast<int64_t>(nsm) * per_sm);
 }
 
 bool launch_column_sum(const float* part, int64_t P, int n, int n0, float* out0, float* out1, cudaStream_t s) {
@@ -370,19 +370,29 @@ sdattn_status check_adapter(const sdattn_adapter_desc* d) {
   return SDATTN_OK;
 }
 
+// Whether the adapters are per-row work: requests of fewer than 16 rows, and D
+// and U read anew for every row are at most 64 MB (about 8 us out of L2).
+bool adapter_rows(const sdattn_adapter_desc* d) {
+  return d->L > 0 && d->rows < 16 && d->T * d->R * (static_cast<int64_t>(d->C) + d->K) * 2 <= (int64_t(64) << 20);
+}
+
+size_t adapter_ws_bytes(const sdattn_adapter_desc* d) {
+  return adapter_rows(d) ? static_cast<size_t>(d->T) * d->R * sizeof(float) : 0;
+}
+
 // Columns per tile (a multiple of 16 up to 192): the fewest waves of the
 // longer of a tile's products (2 clocks per column and 64 of C, the adapters'
-// ranks included) and loads (64 bytes per clock and SM), its epilogue beside
+// ranks included) and loads (45 bytes per clock and SM), its epilogue beside
 // them, plus one epilogue at the end.
-int plan_adapter(const sdattn_adapter_desc* d, int rc, int nsm) {
-  const int64_t rts = (d->T + 127) / 128;
+int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int nsm) {
+  const int64_t rts = (d->T + tm - 1) / tm;
   const double ksteps = (d->C + 63) / 64;
   int best_bn = sdattn::AdapterCfg::BN;
   double best = 1e300;
   for (int bn = sdattn::AdapterCfg::BN; bn >= 16; bn -= 16) {
     const int64_t tiles = rts * ((d->K + bn - 1) / bn);
     const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
-    const double tile = std::max(ksteps * std::max(2.0 * (bn + rc), 2.0 * (128 + bn + rc)), 8.0 * bn);
+    const double tile = std::max(ksteps * std::max(2.0 * (bn + rc), 128.0 * (tm + bn + rc) / 45.0), 8.0 * bn);
     const double cost = waves * tile + 8.0 * bn;
     if (cost < best) {
       best = cost;
@@ -392,10 +402,11 @@ int plan_adapter(const sdattn_adapter_desc* d, int rc, int nsm) {
   return best_bn;
 }
 
-template <bool BF16>
+template <bool BF16, bool ROWS>
 sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const void* W, const float* bias,
-                             const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
+                             const void* D, const void* U, const float* scale, const int32_t* ids, void* Y, void* ws,
                              cudaStream_t s) {
+  using Cfg = sdattn::AdapterCfg;
   const int dev = current_device();
   if (dev < 0) return SDATTN_ERR_CUDA;
   const int nsm = sm_count(dev);
@@ -404,32 +415,44 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.bias = bias;
   p.ids = ids;
   p.scale = scale;
+  p.z = static_cast<const float*>(ws);
+  p.U = U;
   p.Y = Y;
   p.T = static_cast<int>(T);
   p.K = d->K;
   p.L = ids ? d->L : 0;
+  p.R = d->R;
   p.rows = d->rows;
+  const bool mma = ids && !ROWS;                    // adapters on the tensor cores
   p.rc = std::max(16, std::min(64, (d->R + 15) / 16 * 16));
   p.chunks = std::max(1, (d->R + 63) / 64);
-  p.bn = plan_adapter(d, ids ? p.rc : 0, nsm);
-  p.tm = 128;
+  p.tm = static_cast<int>(std::min<uint64_t>(128, (T + 7) / 8 * 8));
+  p.bn = plan_adapter(d, p.tm, mma ? p.rc : 0, nsm);
   p.rts = static_cast<int>((T + p.tm - 1) / p.tm);
   p.nts = (d->K + p.bn - 1) / p.bn;
   p.ksteps = (d->C + 63) / 64;
+  p.stage = p.tm * 128 + p.bn * 128 + (mma ? Cfg::ZN * 128 : 0);
+  p.stages = std::min(Cfg::MAX_STAGES, (Cfg::RING - (p.tm < 128 ? Cfg::SLACK : 0)) / p.stage);
   const CUtensorMapDataType dt = elem16(d->dtype);
   CUtensorMap mx, mw, md, mu;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, K, 1, C * 2, K * C * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
-  if (ids) {
+  if (mma) {
     if (!make_map_3d(&md, D, dt, C, R, L, C * 2, R * C * 2, 64, static_cast<uint32_t>(p.rc))) return SDATTN_ERR_CUDA;
     if (!make_map_3d(&mu, U, dt, R, K, L, R * 2, K * R * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
   } else {
     md = mu = mw;   // never read
   }
-  auto kern = sdattn::adapter_kernel<BF16>;
+  if constexpr (ROWS) {
+    const int64_t warps = d->T * (d->R / 2);
+    if (!launch(sdattn::adapter_z_kernel<BF16>, static_cast<int>((warps + 7) / 8), 256, 0, s,
+                static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(D), scale, ids, static_cast<float*>(ws),
+                p.T, d->C, d->L, d->R, d->rows))
+      return SDATTN_ERR_CUDA;
+  }
+  auto kern = sdattn::adapter_kernel<BF16, ROWS>;
   static std::atomic<uint64_t> done{0};
-  if (!ensure_smem(kern, sdattn::AdapterCfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
+  if (!ensure_smem(kern, Cfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.nts));
-  return launch(kern, grid, sdattn::AdapterCfg::NTHREADS, sdattn::AdapterCfg::SMEM, s, mx, mw, md, mu, p) ? SDATTN_OK
-                                                                                                          : SDATTN_ERR_CUDA;
+  return launch(kern, grid, Cfg::NTHREADS, Cfg::SMEM, s, mx, mw, md, mu, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
   using El = LNElem<DT, VEC>;
   constexpr int E = El::E;
   __shared__ float red[32];
-  extern __shared__ float colsum[];   // [2C], warp kernels only
+  extern __shared__ __align__(16) float colsum[];   // [warps][C], warp kernels only
   const int lane = CTA ? threadIdx.x : threadIdx.x & (p.L - 1);
   const int rpc = CTA ? 1 : blockDim.x / p.L;
   const int grp = CTA ? 0 : threadIdx.x / p.L;
@@ -289,25 +289,34 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
           ag[u][e] += __shfl_xor_sync(0xffffffffu, ag[u][e], off);
           ab[u][e] += __shfl_xor_sync(0xffffffffu, ab[u][e], off);
         }
-    const int warp = threadIdx.x >> 5;
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-      if (warp == w && static_cast<int>(threadIdx.x & 31) < p.L) {
+    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {        // dgamma's sums, then dbeta's
+      if (static_cast<int>(threadIdx.x & 31) < p.L) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int i = lane + u * p.L;
-          if (i < p.nch)
+          if (i < p.nch) {
+            const float* a = side ? ab[u] : ag[u];
+            float* d = colsum + warp * p.C + i * E;
+            if constexpr (VEC) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              float* a = colsum + i * E + e;
-              float* b = a + p.C;
-              *a = w == 0 ? ag[u][e] : *a + ag[u][e];
-              *b = w == 0 ? ab[u][e] : *b + ab[u][e];
+              for (int q = 0; q < E / 4; ++q)
+                reinterpret_cast<float4*>(d)[q] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+            } else {
+              *d = a[0];
             }
+          }
         }
       }
       __syncthreads();
+      for (int j = threadIdx.x; j < p.C; j += blockDim.x) {
+        float t = colsum[j];
+        for (int w = 1; w < nw; ++w) t += colsum[w * p.C + j];
+        out[side * p.C + j] = t;
+      }
+      __syncthreads();
     }
-    for (int j = threadIdx.x; j < 2 * p.C; j += blockDim.x) out[j] = colsum[j];
   }
 }
 

@@ -1198,9 +1198,14 @@ sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, co
                                     : launch_ff_bwd<false>(desc, pl, dY, X, W, bias, dX, dW, dbias, ws, s);
 }
 
+size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc) {
+  if (check_adapter(desc) != SDATTN_OK) return 0;
+  return adapter_ws_bytes(desc);
+}
+
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
                                     const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
-                                    void* stream) {
+                                    void* ws, size_t ws_bytes, void* stream) {
   const sdattn_status st = check_adapter(desc);
   if (st != SDATTN_OK) return st;
   if (desc->T == 0) return SDATTN_OK;
@@ -1209,9 +1214,17 @@ sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void*
   if (!aligned16(X) || !aligned16(W) || !aligned16(bias) || !aligned16(D) || !aligned16(U) || !aligned16(Y) ||
       !aligned_to(scale, 4) || !aligned_to(ids, 4))
     return SDATTN_ERR_ALIGNMENT;
+  const bool rows = ids != nullptr && adapter_rows(desc), bf16 = desc->dtype == SDATTN_BF16;
+  if (rows) {
+    if (!ws || ws_bytes < adapter_ws_bytes(desc)) return SDATTN_ERR_WORKSPACE;
+    if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SDATTN_BF16 ? launch_adapter<true>(desc, X, W, bias, D, U, scale, ids, Y, s)
-                                    : launch_adapter<false>(desc, X, W, bias, D, U, scale, ids, Y, s);
+  if (rows)
+    return bf16 ? launch_adapter<true, true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s)
+                : launch_adapter<false, true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s);
+  return bf16 ? launch_adapter<true, false>(desc, X, W, bias, D, U, scale, ids, Y, nullptr, s)
+              : launch_adapter<false, false>(desc, X, W, bias, D, U, scale, ids, Y, nullptr, s);
 }
 
 const char* sdattn_status_string(sdattn_status status) {

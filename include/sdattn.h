@@ -403,21 +403,28 @@ typedef struct {
     int32_t dtype;    /* sdattn_dtype of X, W, D, U and Y */
 } sdattn_adapter_desc;
 
+/* Bytes of workspace sdattn_adapter_linear needs for this shape with ids; 0
+ * when it needs none, and for an invalid desc. */
+size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc);
+
 /* A projection shared by many requests, each with a low-rank adapter of its
- * own, in one launch: with i = ids[t / rows],
+ * own: with i = ids[t / rows],
  *   Y[t] = X[t] W^T + bias + scale[i] (X[t] D[i]^T) U[i]^T     if 0 <= i < L,
  *   Y[t] = X[t] W^T + bias                                     otherwise
- * (16-bit products with fp32 sums; scale[i] X D[i]^T is rounded to dtype once,
- * as the second product's operand; Y is rounded once).  X, W: inputs; bias:
+ * (16-bit products with fp32 sums, Y rounded once).  X, W: inputs; bias:
  * float32 [K] or NULL; ids: int32 [T / rows] in device memory, or NULL for the
  * plain projection (then D, U and scale must be NULL too); scale: float32 [L]
- * or NULL (ones).  Requests may name adapters in any order and share them;
- * the call is cheapest when neighbouring requests share one, since each
- * distinct adapter among a tile's 128 rows costs it one more small product.
- * T = 0 does nothing. */
+ * or NULL (ones).  Requests may name adapters in any order and share them.
+ * Requests of many rows run in one launch, in which scale[i] X D[i]^T is
+ * rounded to dtype once, as the second product's operand, and each distinct
+ * adapter among a tile's 128 rows costs one more small product; requests of
+ * fewer than 16 rows, while D and U read once per row stay below 64 MB, run
+ * in two launches through ws (16-byte aligned, caller-owned, overwritten, no
+ * state between calls; else NULL / 0 will do), without that rounding.  T = 0
+ * does nothing. */
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
                                     const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
-                                    void* stream);
+                                    void* ws, size_t ws_bytes, void* stream);
 
 /* Reads and clears this device's error word (synchronises the device).
  * Returns SDATTN_OK, SDATTN_ERR_TIMEOUT, or SDATTN_ERR_CUDA if it cannot be

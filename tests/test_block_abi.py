@@ -104,16 +104,26 @@ def ad(T=64, C=320, K=320, L=2, R=16, rows=32, dtype=0):
                                        (dict(rows=48), 1), (dict(L=0), 1), (dict(R=0), 1), (dict(C=12), 2), (dict(K=20), 2),
                                        (dict(R=4), 2), (dict(R=264), 2), (dict(dtype=2), 2), (dict(T=1 << 27), 2)])
 def test_adapter_descriptor(lib, kw, status):
-    assert lib.sdattn_adapter_linear(ad(**kw), OK, OK, OK, OK, OK, OK, OK, OK, None) == status
+    assert lib.sdattn_adapter_linear(ad(**kw), OK, OK, OK, OK, OK, OK, OK, OK, None, 0, None) == status
+    assert lib.sdattn_adapter_linear_workspace_bytes(ad(**kw)) == 0
 
 
 def test_adapter_pointers(lib):
-    f = lib.sdattn_adapter_linear
-    assert f(None, OK, OK, OK, OK, OK, OK, OK, OK, None) == 1
+    def f(d, *ptrs, ws=None, n=0):
+        return lib.sdattn_adapter_linear(d, *ptrs, ws, n, None)
+
+    assert f(None, OK, OK, OK, OK, OK, OK, OK, OK) == 1
     for k in (0, 1, 3, 4, 7):                      # X, W, D, U, Y
-        assert f(ad(), *[None if i == k else OK for i in range(8)], None) == 1
-        assert f(ad(), *[OFF4 if i == k else OK for i in range(8)], None) == 3
-    assert f(ad(), OK, OK, OK, OK, OK, OK, None, OK, None) == 1              # adapters without ids
-    assert f(ad(L=0, R=0), OK, OK, OK, OK, OK, OK, OK, OK, None) == 1        # ids without adapters
-    assert f(ad(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK, None) == 3
-    assert f(ad(T=0), *[None] * 8, None) == 0
+        assert f(ad(), *[None if i == k else OK for i in range(8)]) == 1
+        assert f(ad(), *[OFF4 if i == k else OK for i in range(8)]) == 3
+    assert f(ad(), OK, OK, OK, OK, OK, OK, None, OK) == 1              # adapters without ids
+    assert f(ad(L=0, R=0), OK, OK, OK, OK, OK, OK, OK, OK) == 1        # ids without adapters
+    assert f(ad(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK) == 3
+    assert f(ad(T=0), *[None] * 8) == 0
+    # requests of a few rows need a workspace: z [T][R] in fp32
+    few = dict(T=48, rows=1, R=32)
+    assert lib.sdattn_adapter_linear_workspace_bytes(ad(**few)) == 48 * 32 * 4
+    assert lib.sdattn_adapter_linear_workspace_bytes(ad()) == 0
+    assert f(ad(**few), *[OK] * 8) == 4
+    assert f(ad(**few), *[OK] * 8, ws=OK, n=48 * 32 * 4 - 1) == 4
+    assert f(ad(**few), *[OK] * 8, ws=OFF4, n=48 * 32 * 4) == 3

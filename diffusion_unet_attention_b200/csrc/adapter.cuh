@@ -32,6 +32,7 @@
 // projection's epilogue adds z U^T, 8 ranks of 32 columns at a time (ROWS).
 #pragma once
 
+#include "pipeline.cuh"
 #include "unet_ops.cuh"
 
 namespace sdattn {
@@ -143,11 +144,12 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile uint32_t* abort_flag = misc + 1;
   AdapterPlan* plans = reinterpret_cast<AdapterPlan*>(smem + C::OFF_PLAN);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int tiles = p.rts * p.nts;
   const int spp = C::ZN / p.rc;               // slots per phase
   const bool planned = !ROWS && p.ids != nullptr;
   const uint32_t NS = p.stages;
+  const uint32_t sbase = smem_u32(smem), bfull = smem_u32(full), bempty = smem_u32(empty);
   const int off_w = p.tm * 128, off_d = off_w + p.bn * 128;
   const int mid = p.ksteps / 2;               // the step of x's products after which the last phase's z U^T goes
 
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     uint32_t ui = 0;
     for (int u = blockIdx.x; planned && u < tiles; u += gridDim.x, ++ui) {
       const uint32_t pb = ui % C::PLANS, n = ui / C::PLANS;
-      if (!mbar_wait_warp(&plan_empty[pb], (n & 1) ^ 1, kSiteTicket, abort_flag)) break;
+      if (!wait_warp(smem_u32(&plan_empty[pb]), (n & 1) ^ 1, kSiteTicket, abort_flag)) break;
       AdapterPlan* pl = &plans[pb];
       const int r0 = u / p.nts * p.tm;
       int id[4];
@@ -236,147 +238,150 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     }
   } else if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
-      uint32_t c = 0, ui = 0;
-      bool live = true, pend = false;
-      int pend_ph = 0, pend_n0 = 0;
-      uint32_t pend_pb = 0;
-      bool pend_last = false;
-      // the U tiles of a phase, one stage per slot
-      auto load_up = [&]() {
-        const AdapterPlan* pl = &plans[pend_pb];
-        const int ns = slots_of(pl->count, pend_ph);
-        for (int j = 0; j < ns && live; ++j, ++c) {
-          const int s = pend_ph * spp + j, a = pl->adapter[s / p.chunks], ch = s % p.chunks;
-          const uint32_t st = c % NS, n = c / NS;
-          if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-          mbar_arrive_expect_tx(&full[st], p.bn * 128);
-          tma_load_3d(smem + st * p.stage + off_w, &tmU, ch * 64, pend_n0, a, &full[st]);
-        }
-        if (pend_last) mbar_arrive(&plan_empty[pend_pb]);
-        pend = false;
-      };
-      for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
-        const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
-        const uint32_t pb = ui % C::PLANS;
-        if (planned && !mbar_wait(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag)) { live = false; break; }
-        const AdapterPlan* pl = &plans[pb];
-        const int count = planned ? pl->count : 0, nph = phases(count);
-        for (int ph = 0; ph < nph && live; ++ph) {
-          const int ns = slots_of(count, ph);
-          const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + max(ns, 0) * p.rc * 128;
-          for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-            const uint32_t st = c % NS, n = c / NS;
-            if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-            uint8_t* s = smem + st * p.stage;
-            mbar_arrive_expect_tx(&full[st], bytes);
-            tma_load_3d(s, &tmX, ks * C::BK, rt * p.tm, 0, &full[st]);
-            if (ph == 0) tma_load_3d(s + off_w, &tmW, ks * C::BK, n0, 0, &full[st]);
+    RingPos at;
+    uint32_t c = 0, ui = 0;
+    bool live = true, pend = false, pend_last = false;
+    int pend_ph = 0, pend_n0 = 0;
+    uint32_t pend_pb = 0;
+    for (int u = blockIdx.x; live; u += gridDim.x, ++ui) {
+      const bool more = u < tiles;              // one turn past the last tile: its last phase's U tiles
+      if (!more && !pend) break;
+      const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
+      const uint32_t pb = ui % C::PLANS;
+      int count = 0;
+      if (more && planned) {
+        live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+        if (!live) break;
+        count = plans[pb].count;
+      }
+      const int nph = more ? phases(count) : 1, steps = more ? p.ksteps : 1;
+      for (int ph = 0; ph < nph && live; ++ph) {
+        const int ns = more ? slots_of(count, ph) : 0;
+        const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + ns * p.rc * 128;
+        for (int ks = 0; ks < steps; ++ks) {
+          if (more) {
+            live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+            if (!live) break;
+            const uint32_t s = sbase + at.st * p.stage, bar = bfull + 8 * at.st;
+            expect_tx_elect(bar, bytes);
+            load_elect(s, &tmX, ks * C::BK, rt * p.tm, 0, bar);
+            if (ph == 0) load_elect(s + off_w, &tmW, ks * C::BK, n0, 0, bar);
             for (int j = 0; j < ns; ++j) {
               const int sl = ph * spp + j;
-              tma_load_3d(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
-                          pl->adapter[sl / p.chunks], &full[st]);
+              load_elect(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
+                         plans[pb].adapter[sl / p.chunks], bar);
             }
-            if (ks == mid && pend) {
-              ++c;                              // this step's stage
-              load_up();
-              if (!live) break;
-              --c;                              // counted by the loop
-            }
+            at.next(NS);
+            ++c;
           }
-          if (ns > 0) {
-            pend = true;
-            pend_ph = ph;
-            pend_n0 = n0;
-            pend_pb = pb;
-            pend_last = ph == nph - 1;
-          } else if (planned) {
-            mbar_arrive(&plan_empty[pb]);       // a tile without adapters
+          if (pend && (ks == mid || !more)) {
+            // the U tiles of the last phase, one stage per slot
+            const AdapterPlan* pl = &plans[pend_pb];
+            const int nu = slots_of(pl->count, pend_ph);
+            for (int j = 0; j < nu; ++j) {
+              live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+              if (!live) break;
+              const int sl = pend_ph * spp + j;
+              const uint32_t bar = bfull + 8 * at.st;
+              expect_tx_elect(bar, p.bn * 128);
+              load_elect(sbase + at.st * p.stage + off_w, &tmU, sl % p.chunks * 64, pend_n0, pl->adapter[sl / p.chunks], bar);
+              at.next(NS);
+              ++c;
+            }
+            if (!live) break;
+            if (pend_last) arrive_elect(smem_u32(&plan_empty[pend_pb]));
+            pend = false;
           }
         }
+        if (ns > 0) {
+          pend = true;
+          pend_ph = ph;
+          pend_n0 = n0;
+          pend_pb = pb;
+          pend_last = ph == nph - 1;
+        } else if (more && planned) {
+          arrive_elect(smem_u32(&plan_empty[pb]));   // a tile without adapters
+        }
       }
-      if (pend && live) load_up();
-      // every load this thread issued lands before the CTA can exit
-      volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < NS && st < c; ++st) {
-        const uint32_t uses = (c - st + NS - 1) / NS;
-        mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
-      }
+      if (!more) break;
+    }
+    // every load lands before the CTA can exit
+    volatile uint32_t never = 0;
+    for (uint32_t st = 0; st < NS && st < c; ++st) {
+      const uint32_t uses = (c - st + NS - 1) / NS;
+      wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc_w = idesc_f16(128, p.bn, BF16, false, false);
-    const uint32_t base = smem_u32(smem);
-    uint32_t c = 0, ui = 0, zc = 0;             // stages, tiles, phases with adapters
-    bool live = true, pend = false;
+    const uint64_t xdesc = sdesc_sw128(sbase, 16, 1024), wdesc = sdesc_sw128(sbase + off_w, 16, 1024);
+    const uint64_t ddesc = sdesc_sw128(sbase + off_d, 16, 1024);
+    RingPos at;
+    uint32_t ui = 0, zc = 0;                    // tiles, phases with adapters
+    bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_count = 0;
     uint32_t pend_pb = 0, pend_ab = 0, pend_z = 0;
-    bool pend_last = false;
-    // z U^T of a phase onto its tile's accumulator
-    auto mma_up = [&]() {
-      const uint32_t zb = pend_z & 1;
-      if (!mbar_wait_warp(&p_full[zb], (pend_z >> 1) & 1, kSitePFull, abort_flag)) { live = false; return; }
-      tc_fence_after();
-      const int ns = slots_of(pend_count, pend_ph);
-      for (int j = 0; j < ns; ++j, ++c) {
-        const uint32_t st = c % NS, n = c / NS;
-        if (!mbar_wait_warp(&full[st], n & 1, kSiteVFull, abort_flag)) { live = false; return; }
-        tc_fence_after();
-        const uint32_t su = base + st * p.stage + off_w;
-        for (int kk = 0; kk < p.rc / 16; ++kk) {
-          const int r = j * p.rc + kk * 16;     // rank within the phase: two per tensor-memory column
-          mma_ts(tmem + pend_ab * C::BN, tmem + C::TM_Z + zb * C::ZN + r / 32 * 32 + r % 32 / 2,
-                 sdesc_sw128(su + kk * 32, 16, 1024), idesc_w, 1u);
+    for (int u = blockIdx.x; live; u += gridDim.x, ++ui) {
+      const bool more = u < tiles;              // as in the producer
+      if (!more && !pend) break;
+      const uint32_t ab = ui & 1, na = ui >> 1, pb = ui % C::PLANS;
+      int count = 0;
+      if (more) {
+        if (planned) {
+          live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+          if (!live) break;
+          count = plans[pb].count;
         }
-        mma_commit(&empty[st]);
+        live = wait_warp(smem_u32(&acc_empty[ab]), (na & 1) ^ 1, kSiteAccEmpty, abort_flag);
+        if (!live) break;
+        tc_fence_after();
       }
-      if (pend_last) {
-        mma_commit(&acc_full[pend_ab]);
-        if (lane == 0) mbar_arrive(&plan_empty[pend_pb]);
-      }
-      pend = false;
-    };
-    for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
-      const uint32_t ab = ui & 1, na = ui >> 1;
-      const uint32_t pb = ui % C::PLANS;
-      if (planned && !mbar_wait_warp(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag)) { live = false; break; }
-      const int count = planned ? plans[pb].count : 0, nph = phases(count);
-      if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
-      tc_fence_after();
+      const int nph = more ? phases(count) : 1, steps = more ? p.ksteps : 1;
       for (int ph = 0; ph < nph && live; ++ph) {
-        const int ns = slots_of(count, ph);
+        const int ns = more ? slots_of(count, ph) : 0;
         const uint32_t zb = zc & 1;
         const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
-        for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-          const uint32_t st = c % NS, n = c / NS;
-          if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
-          tc_fence_after();
-          const uint32_t s = base + st * p.stage;
-#pragma unroll
-          for (int kk = 0; kk < C::BK / 16; ++kk) {
-            const uint64_t xd = sdesc_sw128(s + kk * 32, 16, 1024);
-            const uint32_t acc = (ks > 0 || kk > 0) ? 1u : 0u;
-            if (ph == 0) mma_ss(tmem + ab * C::BN, xd, sdesc_sw128(s + off_w + kk * 32, 16, 1024), idesc_w, acc);
-            if (ns > 0)
-              mma_ss(tmem + C::TM_Z + zb * C::ZN, xd, sdesc_sw128(s + off_d + kk * 32, 16, 1024),
-                     idesc_d, acc);
-          }
-          mma_commit(&empty[st]);
-          if (ks == mid && pend) {
-            ++c;
-            mma_up();
+        for (int ks = 0; ks < steps; ++ks) {
+          if (more) {
+            live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
             if (!live) break;
-            --c;
+            tc_fence_after();
+            const uint64_t off = at.st * (p.stage >> 4);
+            if (ph == 0) mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
+            if (ns > 0) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
+            mma_commit_at(bempty + 8 * at.st);
+            at.next(NS);
+          }
+          if (pend && (ks == mid || !more)) {
+            // z U^T of the last phase onto its tile's accumulator
+            const uint32_t pz = pend_z & 1;
+            live = wait_warp(smem_u32(&p_full[pz]), (pend_z >> 1) & 1, kSitePFull, abort_flag);
+            if (!live) break;
+            tc_fence_after();
+            const int nu = slots_of(pend_count, pend_ph);
+            for (int j = 0; j < nu; ++j) {
+              live = wait_warp(bfull + 8 * at.st, at.use, kSiteVFull, abort_flag);
+              if (!live) break;
+              tc_fence_after();
+              const uint64_t ud = wdesc + at.st * (p.stage >> 4);
+              for (int kk = 0; kk < p.rc / 16; ++kk) {
+                const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column
+                mma_ts(tmem + pend_ab * C::BN, tmem + C::TM_Z + pz * C::ZN + r / 32 * 32 + r % 32 / 2, ud + 2 * kk, idesc_w, 1u);
+              }
+              mma_commit_at(bempty + 8 * at.st);
+              at.next(NS);
+            }
+            if (!live) break;
+            if (pend_last) {
+              mma_commit_at(smem_u32(&acc_full[pend_ab]));
+              arrive_elect(smem_u32(&plan_empty[pend_pb]));
+            }
+            pend = false;
           }
         }
-        if (!live) break;
+        if (!live || !more) break;
         if (ns > 0) {
-          mma_commit(&z_full[zb]);
-        } else {
-          mma_commit(&acc_full[ab]);
-          if (planned && lane == 0) mbar_arrive(&plan_empty[pb]);
-        }
-        if (ns > 0) {
+          mma_commit_at(smem_u32(&z_full[zb]));
           pend = true;
           pend_ph = ph;
           pend_count = count;
@@ -384,13 +389,16 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           pend_ab = ab;
           pend_z = zc++;
           pend_last = ph == nph - 1;
+        } else {
+          mma_commit_at(smem_u32(&acc_full[ab]));
+          if (planned) arrive_elect(smem_u32(&plan_empty[pb]));
         }
       }
+      if (!more) break;
     }
-    if (pend && live) mma_up();
     volatile uint32_t never = 0;
-    mma_commit(drain_bar);
-    mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+    mma_commit_at(smem_u32(drain_bar));
+    wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
   } else if (warp >= 4) {
     // ------------------------------ epilogue ----------------------------------
     const int quarter = warp & 3, half = (warp - 4) >> 2;
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       float scale = 0.f;
       if (planned) {
         const uint32_t pb = ui % C::PLANS;
-        live = mbar_wait_warp(&plan_full[pb], (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+        live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
         if (!live) break;
         const AdapterPlan* pl = &plans[pb];
         count = pl->count;
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const int nph = phases(count);
         for (int ph = 0; ph < nph; ++ph, ++zc) {
           const uint32_t zb = zc & 1;
-          live = mbar_wait_warp(&z_full[zb], (zc >> 1) & 1, kSiteSFull, abort_flag);
+          live = wait_warp(smem_u32(&z_full[zb]), (zc >> 1) & 1, kSiteSFull, abort_flag);
           if (!live) break;
           tc_fence_after();
           const uint32_t zt = tmem + C::TM_Z + zb * C::ZN + half * 32 + lane_off;
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         }
         if (!live) break;
       }
-      live = mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag);
+      live = wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag);
       if (!live) break;
       tc_fence_after();
       // 32 columns at a time (the last ones 16), the two warps of a quarter in turn

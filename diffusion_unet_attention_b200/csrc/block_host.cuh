@@ -226,6 +226,11 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   p.rts = static_cast<int>(plan.pair ? (T + 255) / 256 : (T + 127) / 128);
   p.fts = (d->F + p.hn - 1) / p.hn;
   p.ksteps = (d->C + 63) / 64;
+  // The tensor cores' fp32 sums truncate: an entry of h or g comes out low by
+  // about 1.2e-9 of its terms per column of C, which all rows share and db
+  // adds up (1.5e-6 of db at C = 1280).  Past C = 640 the backward pass halves
+  // that with two chains per tile, whose sums are rounded once.
+  p.chains = BWD && p.ksteps > 10 ? 2 : 1;
   const CUtensorMapDataType dt = elem16(d->dtype);
   CUtensorMap mx, mw, my;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 128)) return SDATTN_ERR_CUDA;
@@ -259,7 +264,7 @@ struct FFBwdPlan {
 };
 
 // A result's columns are cut into the fewest tiles of at most 256, rounded up
-// to whole slabs of 64.  With L the contraction steps an SM would run if both
+// to whole slabs of 64.  With L the contraction steps a pair of SMs would run if both
 // products were shared out evenly, a contraction longer than 3/4 L is split
 // into pieces of about L / 2 (at least 8 steps: a piece costs a partial
 // result that is written and read again).
@@ -274,11 +279,11 @@ FFBwdPlan plan_ff_bwd(const sdattn_ff_desc* d, int nsm) {
     const int n = (s.N + 255) / 256;
     s.bn = ((s.N + n - 1) / n + 63) / 64 * 64;
     s.nts = (s.N + s.bn - 1) / s.bn;
-    s.mn = (s.M + 127) / 128 * s.nts;
+    s.mn = (s.M + 255) / 256 * s.nts;
     s.ksteps = (K[i] + 63) / 64;
     total += static_cast<double>(s.mn) * s.ksteps;
   }
-  const double L = total / nsm;
+  const double L = total / (nsm / 2);
   size_t at = 0;
   auto place = [&](size_t bytes) { at += (bytes + 255) / 256 * 256; return bytes; };
   pl.p_bytes = place(static_cast<size_t>(d->T) * 2 * d->F * 2);
@@ -338,8 +343,8 @@ sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const 
   auto kern = sdattn::product_kernel<BF16>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, sdattn::ProductCfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
-  const int grid = std::min(nsm, pl.pp.s[0].units + pl.pp.s[1].units);
-  if (!launch(kern, grid, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
+  const int grid = std::min(nsm / 2, pl.pp.s[0].units + pl.pp.s[1].units) * 2;
+  if (!launch_cluster(kern, grid, 2, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
     return SDATTN_ERR_CUDA;
   for (int i = 0; i < 2; ++i) {
     const sdattn::ProductSide& sd = pl.pp.s[i];

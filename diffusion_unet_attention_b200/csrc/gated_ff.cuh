@@ -28,6 +28,7 @@
 // g_f in the same tensor-memory lane, HN columns apart.
 #pragma once
 
+#include "pipeline.cuh"
 #include "unet_ops.cuh"
 
 namespace sdattn {
@@ -96,68 +97,6 @@ __device__ __forceinline__ float warp_column_sums(float* v, int lane) {
   return t;
 }
 
-// ---------------------------------------------------------------------------
-// CTA pairs (cta_group::2): the two CTAs of a cluster, on neighbouring SMs,
-// run one tcgen05.mma of twice the rows.  Each holds its own 128 rows of A and
-// half of B's rows, so a tile of 256 rows reads B from L2 once instead of
-// twice.  The even CTA (the leader) issues the MMAs; barriers that the other
-// CTA signals are addressed in the leader's shared memory.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t rank) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-  return remote;
-}
-
-// A TMA load into this CTA's shared memory that signals the leader's barrier.
-__device__ __forceinline__ void tma_load_3d_pair(void* sdst, const CUtensorMap* map, int x, int y, int z,
-                                                 uint32_t leader_bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(sdst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_result, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_result)),
-               "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, issued by the leader.
-__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrives once on the barrier at this offset in both CTAs when every MMA the
-// elected thread issued so far has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
 struct GatedCfg {
   static constexpr int BK = 64;                     // columns of C per stage
   static constexpr int A_BYTES = 128 * 128;         // 128 rows of x
@@ -191,6 +130,7 @@ struct GatedParams {
   int hn;               // columns of h per tile: a multiple of 16, at most 128
   int rts, fts;         // row tiles (of 256 rows in a pair), column tiles
   int ksteps;           // ceil(C / 64)
+  int chains;           // accumulators a tile's contraction is dealt over: 1, or 2 (backward, long contractions)
 };
 
 // y (or dh and dg) of 8 columns of one row, from the accumulators and the
@@ -253,7 +193,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   float* sbias = reinterpret_cast<float*>(smem + S::OFF_BIAS);
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);   // [0] tensor memory, [1] abort
   volatile uint32_t* abort_flag = misc + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int hn = PAIR ? 128 : p.hn;
   const int tiles = p.rts * p.fts;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
@@ -296,91 +236,103 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
+  const uint32_t sbase = smem_u32(smem), bfull = smem_u32(full), bempty = smem_u32(empty);
+  const uint32_t bacc_full = smem_u32(acc_full), bacc_empty = smem_u32(acc_empty);
+  const int chains = BWD ? p.chains : 1;
+
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
-      const uint32_t bytes = PAIR ? 2 * (C::A_BYTES + 128 * 128) : C::A_BYTES + 2 * hn * 128;
-      uint32_t c = 0;
-      bool live = true;
-      for (int u = u0; u < tiles && live; u += ustep) {
-        const int rt = u / p.fts, ft = u - rt * p.fts;
-        for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-          const uint32_t st = c % S::STAGES, n = c / S::STAGES;
-          if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-          uint8_t* s = smem + st * S::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
-          if constexpr (PAIR) {
-            const uint32_t bar = cluster_addr(&full[st], 0);
-            tma_load_3d_pair(s, &tmX, ks * C::BK, rt * TROWS + rank * 128, 0, bar);
-            tma_load_3d_pair(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, rank, bar);
-          } else {
-            tma_load_3d(s, &tmX, ks * C::BK, rt * TROWS, 0, &full[st]);
-            tma_load_3d(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, &full[st]);
-            tma_load_3d(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, &full[st]);
-          }
+    const uint32_t bytes = PAIR ? 2 * (C::A_BYTES + 128 * 128) : C::A_BYTES + 2 * hn * 128;
+    const uint32_t lfull = PAIR ? cluster_addr(bfull, 0) : bfull;
+    RingPos at;
+    uint32_t c = 0;
+    bool live = true;
+    for (int u = u0; u < tiles && live; u += ustep) {
+      const int rt = u / p.fts, ft = u - rt * p.fts;
+      for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
+        live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+        if (!live) break;
+        const uint32_t s = sbase + at.st * S::STAGE, bar = lfull + 8 * at.st;
+        if (rank == 0) expect_tx_elect(bfull + 8 * at.st, bytes);
+        if constexpr (PAIR) {
+          load_elect_pair(s, &tmX, ks * C::BK, rt * TROWS + rank * 128, 0, bar);
+          load_elect_pair(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, rank, bar);
+        } else {
+          load_elect(s, &tmX, ks * C::BK, rt * TROWS, 0, bar);
+          load_elect(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, bar);
+          load_elect(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, bar);
         }
+        at.next(S::STAGES);
       }
-      // every load lands before the CTA (or its pair) can exit
-      if (rank == 0) {
-        volatile uint32_t never = 0;
-        for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
-          const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
-          mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
-        }
+    }
+    // every load lands before the CTA (or its pair) can exit
+    if (rank == 0) {
+      volatile uint32_t never = 0;
+      for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
+        const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
+        wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
       }
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc = idesc_f16(TROWS, 2 * hn, BF16, false, false);
-    const uint32_t base = smem_u32(smem);
-    uint32_t c = 0, ui = 0;
+    const uint64_t adesc = sdesc_sw128(sbase, 16, 1024), bdesc = sdesc_sw128(sbase + C::A_BYTES, 16, 1024);
+    RingPos at;
+    uint32_t ui = 0;
     bool live = true;
     for (int u = u0; u < tiles && live; u += ustep, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
-      if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
+      // one chain: tiles alternate between the accumulators, and this one was
+      // the tile's before last; two: every tile takes both, after the last one
+      if (chains == 1) {
+        live = wait_warp(bacc_empty + 8 * ab, (na & 1) ^ 1, kSiteAccEmpty, abort_flag);
+      } else if (ui > 0) {
+        live = wait_warp(bacc_empty + 8 * (ab ^ 1), ((ui - 1) >> 1) & 1, kSiteAccEmpty, abort_flag);
+      }
+      if (!live) break;
       tc_fence_after();
-      for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-        const uint32_t st = c % S::STAGES, n = c / S::STAGES;
-        if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
+      const int turn = chains == 1 ? p.ksteps : (p.ksteps + 1) / 2;
+      uint32_t d = tmem + (chains == 1 ? ab * 256 : 0), acc = 0;
+      for (int ks = 0; ks < p.ksteps; ++ks) {
+        live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
+        if (!live) break;
         tc_fence_after();
-        const uint32_t s = base + st * S::STAGE;
-#pragma unroll
-        for (int kk = 0; kk < C::BK / 16; ++kk) {
-          const uint64_t ad = sdesc_sw128(s + kk * 32, 16, 1024), bd = sdesc_sw128(s + C::A_BYTES + kk * 32, 16, 1024);
-          const uint32_t acc = (ks > 0 || kk > 0) ? 1u : 0u;
-          if constexpr (PAIR) {
-            mma_ss_pair(tmem + ab * 256, ad, bd, idesc, acc);
-          } else {
-            mma_ss(tmem + ab * 256, ad, bd, idesc, acc);
-          }
+        if (BWD && ks == turn) {
+          d = tmem + 256;
+          acc = 0;
         }
+        const uint64_t off = at.st * (S::STAGE >> 4);
         if constexpr (PAIR) {
-          mma_commit_pair(&empty[st]);
+          mma_ss4_pair(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
+          mma_commit_pair(bempty + 8 * at.st);
         } else {
-          mma_commit(&empty[st]);
+          mma_ss4(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
+          mma_commit_at(bempty + 8 * at.st);
         }
+        acc = 1;
+        at.next(S::STAGES);
       }
       if (live) {
         if constexpr (PAIR) {
-          mma_commit_pair(&acc_full[ab]);
+          mma_commit_pair(bacc_full + 8 * ab);
         } else {
-          mma_commit(&acc_full[ab]);
+          mma_commit_at(bacc_full + 8 * ab);
         }
       }
     }
     volatile uint32_t never = 0;
     if constexpr (PAIR) {
-      mma_commit_pair(drain_bar);
+      mma_commit_pair(smem_u32(drain_bar));
     } else {
-      mma_commit(drain_bar);
+      mma_commit_at(smem_u32(drain_bar));
     }
-    mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+    wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
   } else if (warp == 2) {
     // ------------------------------ biases ------------------------------------
     uint32_t ui = 0;
     for (int u = u0; u < tiles; u += ustep, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
-      if (!mbar_wait_warp(&bias_empty[ab], (na & 1) ^ 1, kSiteVEmpty, abort_flag)) break;
+      if (!wait_warp(smem_u32(&bias_empty[ab]), (na & 1) ^ 1, kSiteVEmpty, abort_flag)) break;
       const int f = (u % p.fts) * hn;
       for (int j = lane; j < hn; j += 32) {
         const bool ok = p.bias != nullptr && f + j < p.F;   // columns past F take none: their products are zero
@@ -403,8 +355,8 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
       const int r0 = rt * TROWS + rank * 128 + quarter * 32, row = r0 + lane;
       const bool row_ok = row < p.T;
       const uint16_t* dy_row = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + ft * hn;
-      if (!mbar_wait_warp(&bias_full[ab], na & 1, kSiteVFull, abort_flag) ||
-          !mbar_wait_warp(&acc_full[ab], na & 1, kSiteAccFull, abort_flag))
+      if (!wait_warp(smem_u32(&bias_full[ab]), na & 1, kSiteVFull, abort_flag) ||
+          !wait_warp(bacc_full + 8 * ab, na & 1, kSiteAccFull, abort_flag))
         break;
       tc_fence_after();
       // PAIR: this warp's 64 columns; otherwise every other 8 columns
@@ -419,7 +371,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
             dy[q] = row_ok && f + 8 * q < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c0) + q) : make_uint4(0, 0, 0, 0);
         }
         uint32_t h[CW], g[CW];
-        const uint32_t at = tmem + ab * 256 + c0 + lane_off;
+        const uint32_t at = tmem + (chains == 1 ? ab * 256 : 0) + c0 + lane_off;
         if constexpr (PAIR) {
           tmem_ld_x16(at, h);
           tmem_ld_x16(at + hn, g);
@@ -430,6 +382,24 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         tmem_wait_ld();
         reg_fence<CW>(h);
         reg_fence<CW>(g);
+        if (BWD && chains == 2) {                 // the second chain's sums
+          uint32_t h2[CW], g2[CW];
+          if constexpr (PAIR) {
+            tmem_ld_x16(at + 256, h2);
+            tmem_ld_x16(at + 256 + hn, g2);
+          } else {
+            tmem_ld_x8(at + 256, h2);
+            tmem_ld_x8(at + 256 + hn, g2);
+          }
+          tmem_wait_ld();
+          reg_fence<CW>(h2);
+          reg_fence<CW>(g2);
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            h[j] = __float_as_uint(__uint_as_float(h[j]) + __uint_as_float(h2[j]));
+            g[j] = __float_as_uint(__uint_as_float(g[j]) + __uint_as_float(g2[j]));
+          }
+        }
         const float* bh = sbias + ab * 256 + c0;
         float o0[CW], o1[CW];
 #pragma unroll
@@ -492,7 +462,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
       if (lane == 0) {
         mbar_arrive(&bias_empty[ab]);
         if constexpr (PAIR) {
-          mbar_arrive_cluster(cluster_addr(&acc_empty[ab], 0));
+          arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
         } else {
           mbar_arrive(&acc_empty[ab]);
         }
@@ -515,23 +485,24 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// dx = P W and dW = P^T x in one launch.  A unit is a 128-row tile of one of
-// the two results, up to 256 of its columns, over one split of the
-// contraction; units of both results are dealt out in turn, so that neither
-// product leaves SMs idle while the other runs.
+// dx = P W and dW = P^T x in one launch, on CTA pairs.  A unit is a 256-row
+// tile of one of the two results, up to 256 of its columns, over one split of
+// the contraction; units of both results are dealt out in turn, so that
+// neither product leaves SMs idle while the other runs.
 //   dx: A = P [T][2F], K-major;  B = W [2F][C], N-major (its rows run along N)
 //   dW: A = P, M-major (P^T);    B = x [T][C], N-major
-// M- and N-major tiles are slabs of 64 columns x 64 contraction rows, 128-byte
-// swizzled.  A result whose contraction is split goes to fp32 partials that
-// add_splits_kernel adds in split order.
+// Each CTA of a pair holds its 128 rows of A and half of the tile's columns of
+// B.  M- and N-major tiles are slabs of 64 columns x 64 contraction rows,
+// 128-byte swizzled.  A result whose contraction is split goes to fp32
+// partials that add_splits_kernel adds in split order.
 // ---------------------------------------------------------------------------
 struct ProductCfg {
   static constexpr int BK = 64;
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int SLAB = 64 * 128;             // 64 columns x 64 contraction rows
-  static constexpr int BN = 256;                    // most columns of a tile
-  static constexpr int STAGE = A_BYTES + BN / 64 * SLAB;
-  static constexpr int STAGES = 4;
+  static constexpr int BN = 256;                    // most columns of a tile, half of them in each CTA
+  static constexpr int STAGE = A_BYTES + BN / 2 / 64 * SLAB;
+  static constexpr int STAGES = 6;
   static constexpr int OFF_STG = STAGES * STAGE;    // [8 warps] 32 rows x 128 bytes
   static constexpr int OFF_BAR = OFF_STG + 8 * 4096;
   static constexpr int NBAR = 2 * STAGES + 4 + 1;
@@ -545,7 +516,7 @@ struct ProductSide {
   int M, N;           // the result's rows and columns
   int bn;             // columns per tile, a multiple of 64 up to 256
   int nts;            // column tiles
-  int mn;             // row tiles x column tiles
+  int mn;             // row tiles (of 256) x column tiles
   int splits;         // of the contraction
   int ksteps, kper;   // contraction steps of 64: in all, per split
   int units;          // mn * splits
@@ -557,7 +528,7 @@ struct ProductParams {
 };
 
 struct ProductUnit {
-  int side, m0, n0, cols, split, k0, k1;
+  int side, m0, n0, cols, half, split, k0, k1;
 };
 
 __device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, int u) {
@@ -568,9 +539,10 @@ __device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, int 
   const ProductSide& s = p.s[r.side];
   r.split = u / s.mn;
   const int t = u - r.split * s.mn, mt = t / s.nts, nt = t - mt * s.nts;
-  r.m0 = mt * 128;
+  r.m0 = mt * 256;
   r.n0 = nt * s.bn;
   r.cols = min(s.bn, s.N - r.n0);
+  r.half = (r.cols + 31) / 32 * 16;                 // columns of B in each CTA
   r.k0 = r.split * s.kper;
   r.k1 = min(s.ksteps, r.k0 + s.kper);
   return r;
@@ -586,15 +558,16 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* full = bars;
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;
-  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* full = bars;                     // [STAGES] both CTAs' loads -> MMA (the leader's)
+  uint64_t* empty = full + C::STAGES;        // [STAGES] MMA -> TMA
+  uint64_t* acc_full = empty + C::STAGES;    // [2] MMA -> epilogue
+  uint64_t* acc_empty = acc_full + 2;        // [2] both CTAs' epilogues -> MMA (the leader's)
   uint64_t* drain_bar = acc_empty + 2;
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile uint32_t* abort_flag = misc + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = p.s[0].units + p.s[1].units;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int units = p.s[0].units + p.s[1].units, u0 = blockIdx.x / 2, ustep = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -603,7 +576,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], 16);
     }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
@@ -617,88 +590,96 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     tma_prefetch_desc(&tmO0);
     tma_prefetch_desc(&tmO1);
   }
-  if (warp == 1) {
-    tmem_alloc(&misc[0], C::TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_pair(&misc[0], C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                            // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  const uint32_t sbase = smem_u32(smem), bfull = smem_u32(full), bempty = smem_u32(empty);
+  const uint32_t bacc_full = smem_u32(acc_full), bacc_empty = smem_u32(acc_empty);
   grid_dependency_wait();
   grid_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t c = 0;
-      bool live = true;
-      for (int u = blockIdx.x; u < units && live; u += gridDim.x) {
-        const ProductUnit t = product_unit(p, u);
-        const int slabs = (t.cols + 63) / 64;
-        const CUtensorMap* tmB = t.side == 0 ? &tmW : &tmX;
-        for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
-          const uint32_t st = c % C::STAGES, n = c / C::STAGES;
-          if (!mbar_wait(&empty[st], (n & 1) ^ 1, kSiteKEmpty, abort_flag)) { live = false; break; }
-          uint8_t* s = smem + st * C::STAGE;
-          mbar_arrive_expect_tx(&full[st], C::A_BYTES + slabs * C::SLAB);
-          if (t.side == 0) {
-            tma_load_3d(s, &tmPk, ks * C::BK, t.m0, 0, &full[st]);
-          } else {
-            tma_load_3d(s, &tmPm, t.m0, ks * C::BK, 0, &full[st]);
-            tma_load_3d(s + C::SLAB, &tmPm, t.m0 + 64, ks * C::BK, 0, &full[st]);
-          }
-          for (int j = 0; j < slabs; ++j)
-            tma_load_3d(s + C::A_BYTES + j * C::SLAB, tmB, t.n0 + 64 * j, ks * C::BK, 0, &full[st]);
+    // ------------------------------ TMA producer ------------------------------
+    const uint32_t lfull = cluster_addr(bfull, 0);
+    RingPos at;
+    uint32_t c = 0;
+    bool live = true;
+    for (int u = u0; u < units && live; u += ustep) {
+      const ProductUnit t = product_unit(p, u);
+      const int slabs = (t.half + 63) / 64, m = t.m0 + rank * 128, n = t.n0 + rank * t.half;
+      for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
+        live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+        if (!live) break;
+        const uint32_t s = sbase + at.st * C::STAGE, bar = lfull + 8 * at.st;
+        const int k = ks * C::BK;
+        if (rank == 0) expect_tx_elect(bfull + 8 * at.st, 2 * (C::A_BYTES + slabs * C::SLAB));
+        if (t.side == 0) {
+          load_elect_pair(s, &tmPk, k, m, 0, bar);
+          load_elect_pair(s + C::A_BYTES, &tmW, n, k, 0, bar);
+          if (slabs > 1) load_elect_pair(s + C::A_BYTES + C::SLAB, &tmW, n + 64, k, 0, bar);
+        } else {
+          load_elect_pair(s, &tmPm, m, k, 0, bar);
+          load_elect_pair(s + C::SLAB, &tmPm, m + 64, k, 0, bar);
+          load_elect_pair(s + C::A_BYTES, &tmX, n, k, 0, bar);
+          if (slabs > 1) load_elect_pair(s + C::A_BYTES + C::SLAB, &tmX, n + 64, k, 0, bar);
         }
+        at.next(C::STAGES);
       }
+    }
+    if (rank == 0) {
       volatile uint32_t never = 0;
       for (uint32_t st = 0; st < C::STAGES && st < c; ++st) {
         const uint32_t uses = (c - st + C::STAGES - 1) / C::STAGES;
-        mbar_wait(&full[st], (uses - 1) & 1, kSiteKFull, &never);
+        wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
       }
     }
-  } else if (warp == 1) {
-    const uint32_t base = smem_u32(smem);
-    uint32_t c = 0, ui = 0;
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------ MMA issuer --------------------------------
+    RingPos at;
+    uint32_t ui = 0;
     bool live = true;
-    for (int u = blockIdx.x; u < units && live; u += gridDim.x, ++ui) {
+    for (int u = u0; u < units && live; u += ustep, ++ui) {
       const ProductUnit t = product_unit(p, u);
       const uint32_t ab = ui & 1, na = ui >> 1;
-      const uint32_t idesc = idesc_f16(128, (t.cols + 15) / 16 * 16, BF16, t.side == 1, true);
+      const uint32_t idesc = idesc_f16(256, 2 * t.half, BF16, t.side == 1, true);
       // A: 32 bytes along a K-major row, or 16 contraction rows of an M-major slab, per 16 of K
-      const uint32_t a_step = t.side == 1 ? 2048 : 32, a_lbo = t.side == 1 ? C::SLAB : 16;
-      if (!mbar_wait_warp(&acc_empty[ab], (na & 1) ^ 1, kSiteAccEmpty, abort_flag)) { live = false; break; }
+      const uint64_t adesc = sdesc_sw128(sbase, t.side == 1 ? C::SLAB : 16, 1024), astep = t.side == 1 ? 128 : 2;
+      const uint64_t bdesc = sdesc_sw128(sbase + C::A_BYTES, C::SLAB, 1024);
+      live = wait_warp(bacc_empty + 8 * ab, (na & 1) ^ 1, kSiteAccEmpty, abort_flag);
+      if (!live) break;
       tc_fence_after();
-      for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
-        const uint32_t st = c % C::STAGES, n = c / C::STAGES;
-        if (!mbar_wait_warp(&full[st], n & 1, kSiteKFull, abort_flag)) { live = false; break; }
+      uint32_t acc = 0;
+      for (int ks = t.k0; ks < t.k1; ++ks) {
+        live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
+        if (!live) break;
         tc_fence_after();
-        const uint32_t s = base + st * C::STAGE;
-#pragma unroll
-        for (int kk = 0; kk < C::BK / 16; ++kk)
-          mma_ss(tmem + ab * 256, sdesc_sw128(s + kk * a_step, a_lbo, 1024),
-                 sdesc_sw128(s + C::A_BYTES + kk * 2048, C::SLAB, 1024), idesc, (ks > t.k0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[st]);
+        const uint64_t off = at.st * (C::STAGE >> 4);
+        mma_ss4_pair(tmem + ab * 256, adesc + off, bdesc + off, idesc, acc, astep, 128);
+        mma_commit_pair(bempty + 8 * at.st);
+        acc = 1;
+        at.next(C::STAGES);
       }
-      if (live) mma_commit(&acc_full[ab]);
+      if (live) mma_commit_pair(bacc_full + 8 * ab);
     }
     volatile uint32_t never = 0;
-    mma_commit(drain_bar);
-    mbar_wait_warp(drain_bar, 0, kSiteAccFull, &never);
+    mma_commit_pair(smem_u32(drain_bar));
+    wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
   } else if (warp >= 4) {
+    // ------------------------------ epilogue ----------------------------------
     const int quarter = warp & 3, half = (warp - 4) >> 2, ew = warp - 4;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stg = smem + C::OFF_STG + ew * 4096;
     uint32_t ui = 0;
-    bool live = true;
-    for (int u = blockIdx.x; u < units && live; u += gridDim.x, ++ui) {
+    for (int u = u0; u < units; u += ustep, ++ui) {
       const ProductUnit t = product_unit(p, u);
       const ProductSide& sd = p.s[t.side];
       const CUtensorMap* tmO = t.side == 0 ? &tmO0 : &tmO1;
       const uint32_t ab = ui & 1, na = ui >> 1;
-      const int r0 = t.m0 + quarter * 32;
-      live = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], na & 1, kSiteAccFull, abort_flag));
-      if (!live) break;
+      const int r0 = t.m0 + rank * 128 + quarter * 32;
+      if (!wait_warp(bacc_full + 8 * ab, na & 1, kSiteAccFull, abort_flag)) break;
       tc_fence_after();
       const bool f32 = sd.splits > 1;
       const int cw = f32 ? 32 : 64;             // columns per staged piece of 128 bytes
@@ -735,16 +716,17 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      if (lane == 0) arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
     }
     if (lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                            // neither CTA leaves while the other's products read its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc_pair(tmem, C::TMEM_COLS);
   }
 }
 

@@ -41,16 +41,19 @@ struct AdapterCfg {
   static constexpr int BK = 64;
   static constexpr int BN = 192;                    // most columns per tile
   static constexpr int ZN = 64;                     // ranks per phase
-  static constexpr int RING = 217088;               // bytes of the ring of stages
+  static constexpr int RING = 200704;               // bytes of the ring of stages
   static constexpr int SLACK = 16384;               // kept behind it when x's tiles are short: their products read up to 16 KB past a stage
   static constexpr int MAX_STAGES = 20;
   static constexpr int OFF_PLAN = RING;
   static constexpr int PLANS = 4;                   // tiles the planner may run ahead
   static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' places, rows' scales, count
-  static constexpr int OFF_BAR = OFF_PLAN + PLANS * PLAN;
+  static constexpr int OFF_STG = OFF_PLAN + PLANS * PLAN;   // [8 epilogue warps] 32 rows of 32 columns, 80 bytes apart
+  static constexpr int STG = 32 * 80;
+  static constexpr int OFF_BIAS = OFF_STG + 8 * STG;        // [8 epilogue warps] biases of up to 96 columns
+  static constexpr int OFF_BAR = OFF_BIAS + 8 * 96 * 4;
   static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 2 * PLANS + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-  static constexpr int NTHREADS = 384;              // TMA, MMA, planner, idle, eight epilogue warps
+  static constexpr int NTHREADS = 512;              // TMA, MMA, planner, idle, eight epilogue warps, four that convert z
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int TM_Z = 2 * BN;               // accumulators at 0 and BN, z at 384 and 448
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -136,9 +139,9 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   uint64_t* empty = full + C::MAX_STAGES;     // [stages] MMA -> TMA
   uint64_t* acc_full = empty + C::MAX_STAGES; // [2] MMA -> epilogue
   uint64_t* acc_empty = acc_full + 2;         // [2] epilogue -> MMA
-  uint64_t* z_full = acc_empty + 2;           // [2] MMA -> epilogue: z is complete
-  uint64_t* p_full = z_full + 2;              // [2] epilogue -> MMA: z is converted
-  uint64_t* plan_full = p_full + 2;           // [PLANS] planner -> TMA, MMA, epilogue
+  uint64_t* z_full = acc_empty + 2;           // [2] MMA -> conversion: z is complete
+  uint64_t* p_full = z_full + 2;              // [2] conversion -> MMA
+  uint64_t* plan_full = p_full + 2;           // [PLANS] planner -> TMA, MMA, conversion
   uint64_t* plan_empty = plan_full + C::PLANS;   // [PLANS] back
   uint64_t* drain_bar = plan_empty + C::PLANS;
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -162,11 +165,11 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 8);
       mbar_init(&z_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&p_full[i], 4);
     }
     for (int i = 0; i < C::PLANS; ++i) {
       mbar_init(&plan_full[i], 1);
-      mbar_init(&plan_empty[i], 10);
+      mbar_init(&plan_empty[i], 6);
     }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     }
   } else if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    RingPos at;
+    RingWalk ring(bempty, NS, 1);
     uint32_t c = 0, ui = 0;
     bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_n0 = 0;
@@ -260,9 +263,10 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + ns * p.rc * 128;
         for (int ks = 0; ks < steps; ++ks) {
           if (more) {
-            live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+            uint32_t st;
+            live = ring.take(st, kSiteKEmpty, abort_flag);
             if (!live) break;
-            const uint32_t s = sbase + at.st * p.stage, bar = bfull + 8 * at.st;
+            const uint32_t s = sbase + st * p.stage, bar = bfull + 8 * st;
             expect_tx_elect(bar, bytes);
             load_elect(s, &tmX, ks * C::BK, rt * p.tm, 0, bar);
             if (ph == 0) load_elect(s + off_w, &tmW, ks * C::BK, n0, 0, bar);
@@ -271,7 +275,6 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
               load_elect(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
                          plans[pb].adapter[sl / p.chunks], bar);
             }
-            at.next(NS);
             ++c;
           }
           if (pend && (ks == mid || !more)) {
@@ -279,14 +282,14 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             const AdapterPlan* pl = &plans[pend_pb];
             const int nu = slots_of(pl->count, pend_ph);
             for (int j = 0; j < nu; ++j) {
-              live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+              uint32_t st;
+              live = ring.take(st, kSiteKEmpty, abort_flag);
               if (!live) break;
               const int sl = pend_ph * spp + j;
-              const uint32_t bar = bfull + 8 * at.st;
+              const uint32_t bar = bfull + 8 * st;
               expect_tx_elect(bar, p.bn * 128);
-              load_elect(sbase + at.st * p.stage + off_w, &tmU, sl % p.chunks * 64, pend_n0, pl->adapter[sl / p.chunks], bar);
-              at.next(NS);
-              ++c;
+              load_elect(sbase + st * p.stage + off_w, &tmU, sl % p.chunks * 64, pend_n0, pl->adapter[sl / p.chunks], bar);
+                ++c;
             }
             if (!live) break;
             if (pend_last) arrive_elect(smem_u32(&plan_empty[pend_pb]));
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     const uint32_t idesc_w = idesc_f16(128, p.bn, BF16, false, false);
     const uint64_t xdesc = sdesc_sw128(sbase, 16, 1024), wdesc = sdesc_sw128(sbase + off_w, 16, 1024);
     const uint64_t ddesc = sdesc_sw128(sbase + off_d, 16, 1024);
-    RingPos at;
+    RingWalk ring(bfull, NS, 0);
     uint32_t ui = 0, zc = 0;                    // tiles, phases with adapters
     bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_count = 0;
@@ -343,14 +346,14 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
         for (int ks = 0; ks < steps; ++ks) {
           if (more) {
-            live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
+            uint32_t st;
+            live = ring.take(st, kSiteKFull, abort_flag);
             if (!live) break;
             tc_fence_after();
-            const uint64_t off = at.st * (p.stage >> 4);
+            const uint64_t off = st * (p.stage >> 4);
             if (ph == 0) mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
             if (ns > 0) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
-            mma_commit_at(bempty + 8 * at.st);
-            at.next(NS);
+            mma_commit_at(bempty + 8 * st);
           }
           if (pend && (ks == mid || !more)) {
             // z U^T of the last phase onto its tile's accumulator
@@ -360,17 +363,17 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             tc_fence_after();
             const int nu = slots_of(pend_count, pend_ph);
             for (int j = 0; j < nu; ++j) {
-              live = wait_warp(bfull + 8 * at.st, at.use, kSiteVFull, abort_flag);
+              uint32_t st;
+              live = ring.take(st, kSiteVFull, abort_flag);
               if (!live) break;
               tc_fence_after();
-              const uint64_t ud = wdesc + at.st * (p.stage >> 4);
+              const uint64_t ud = wdesc + st * (p.stage >> 4);
               for (int kk = 0; kk < p.rc / 16; ++kk) {
                 const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column
                 mma_ts(tmem + pend_ab * C::BN, tmem + C::TM_Z + pz * C::ZN + r / 32 * 32 + r % 32 / 2, ud + 2 * kk, idesc_w, 1u);
               }
-              mma_commit_at(bempty + 8 * at.st);
-              at.next(NS);
-            }
+              mma_commit_at(bempty + 8 * st);
+              }
             if (!live) break;
             if (pend_last) {
               mma_commit_at(smem_u32(&acc_full[pend_ab]));
@@ -399,49 +402,39 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     volatile uint32_t never = 0;
     mma_commit_at(smem_u32(drain_bar));
     wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
-  } else if (warp >= 4) {
-    // ------------------------------ epilogue ----------------------------------
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+  } else if (warp >= 12) {
+    // ------------------------------ conversion of z ---------------------------
+    const int quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int r = quarter * 32 + lane;
     uint32_t ui = 0, zc = 0;
-    bool live = true;
+    bool live = planned;
     for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
-      const uint32_t ab = ui & 1, na = ui >> 1;
-      const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
-      const int r = quarter * 32 + lane, row = rt * p.tm + r;
-      int count = 0, place = -1;
-      float scale = 0.f;
-      if (planned) {
-        const uint32_t pb = ui % C::PLANS;
-        live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+      const uint32_t pb = ui % C::PLANS;
+      live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
+      if (!live) break;
+      const AdapterPlan* pl = &plans[pb];
+      const int count = pl->count, place = pl->place[r];
+      const float scale = pl->scale[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&plan_empty[pb]);
+      const int nph = count > 0 ? phases(count) : 0;
+      for (int ph = 0; ph < nph; ++ph, ++zc) {
+        const uint32_t zb = zc & 1;
+        live = wait_warp(smem_u32(&z_full[zb]), (zc >> 1) & 1, kSiteSFull, abort_flag);
         if (!live) break;
-        const AdapterPlan* pl = &plans[pb];
-        count = pl->count;
-        place = pl->place[r];
-        scale = pl->scale[r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&plan_empty[pb]);
-      }
-      int id = -1;                              // ROWS: this row's adapter
-      if (ROWS && r < p.tm && row < p.T) {
-        id = __ldg(p.ids + row / p.rows);
-        if (id >= p.L) id = -1;
-      }
-      if (count > 0) {
-        const int nph = phases(count);
-        for (int ph = 0; ph < nph; ++ph, ++zc) {
-          const uint32_t zb = zc & 1;
-          live = wait_warp(smem_u32(&z_full[zb]), (zc >> 1) & 1, kSiteSFull, abort_flag);
-          if (!live) break;
-          tc_fence_after();
-          const uint32_t zt = tmem + C::TM_Z + zb * C::ZN + half * 32 + lane_off;
+        tc_fence_after();
+        const int ranks = slots_of(count, ph) * p.rc;
+#pragma unroll 1
+        for (int j0 = 0; j0 < ranks; j0 += 32) {
+          const uint32_t zt = tmem + C::TM_Z + zb * C::ZN + j0 + lane_off;
           uint32_t v[32], w[16];
           tmem_ld_x32(zt, v);
           tmem_wait_ld();
           reg_fence<32>(v);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {         // 16 ranks belong to one slot
-            const int slot = ph * spp + (half * 32 + g * 16) / p.rc;
+            const int slot = ph * spp + (j0 + g * 16) / p.rc;
             const bool mine = slot / p.chunks == place;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -450,71 +443,91 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
               w[8 * g + j] = pack2<BF16>(a, b);
             }
           }
-          tmem_st_x16(zt, w);                   // over the warp's own columns of z
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[zb]);
+          tmem_st_x16(zt, w);                   // over its own columns of z
         }
-        if (!live) break;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[zb]);
       }
-      live = wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag);
-      if (!live) break;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------ epilogue ----------------------------------
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* stg = smem + C::OFF_STG + (warp - 4) * C::STG;
+    float* sb = reinterpret_cast<float*>(smem + C::OFF_BIAS) + (warp - 4) * 96;
+    uint32_t ui = 0;
+    for (int u = blockIdx.x; u < tiles; u += gridDim.x, ++ui) {
+      const uint32_t ab = ui & 1, na = ui >> 1;
+      const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
+      const int r = quarter * 32 + lane, row = rt * p.tm + r;
+      const int rows = min(min(p.tm - quarter * 32, 32), p.T - rt * p.tm - quarter * 32);   // of this warp
+      __syncwarp();
+      for (int c0 = half * 32, i = lane; c0 < p.bn; c0 += 64, i += 32) {
+        const int n = n0 + c0 + lane;
+        sb[i] = p.bias != nullptr && n < p.K ? __ldg(p.bias + n) : 0.f;
+      }
+      int id = -1;                              // ROWS: this row's adapter
+      if (ROWS && lane < rows) {
+        id = __ldg(p.ids + row / p.rows);
+        if (id >= p.L) id = -1;
+      }
+      __syncwarp();
+      if (!wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag)) break;
       tc_fence_after();
       // 32 columns at a time (the last ones 16), the two warps of a quarter in turn
+      const float* bs = sb;
 #pragma unroll 1
-      for (int c0 = half * 32; c0 < p.bn && n0 + c0 < p.K; c0 += 64) {
+      for (int c0 = half * 32; c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 64, bs += 32) {
         uint32_t v[32];
         tmem_ld_x32(tmem + ab * C::BN + c0 + lane_off, v);
         tmem_wait_ld();
         reg_fence<32>(v);
-        if (r >= p.tm || row >= p.T) continue;
         const int cols = min(min(p.bn - c0, 32), p.K - n0 - c0);   // a multiple of 8
         float f[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        for (int q = 0; q < 8; ++q) {
+          const float4 b = reinterpret_cast<const float4*>(bs)[q];
+          f[4 * q] = __uint_as_float(v[4 * q]) + b.x;
+          f[4 * q + 1] = __uint_as_float(v[4 * q + 1]) + b.y;
+          f[4 * q + 2] = __uint_as_float(v[4 * q + 2]) + b.z;
+          f[4 * q + 3] = __uint_as_float(v[4 * q + 3]) + b.w;
+        }
         if constexpr (ROWS) {
           if (id >= 0) {
             const float4* zr = reinterpret_cast<const float4*>(p.z + static_cast<int64_t>(row) * p.R);
             const uint16_t* up = static_cast<const uint16_t*>(p.U) + (static_cast<int64_t>(id) * p.K + n0 + c0) * p.R;
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {    // 16 loads of U in flight
+            for (int h = 0; h < 32; h += 8) {     // 8 columns' U in flight
               for (int r8 = 0; r8 < p.R && h < cols; r8 += 8) {
                 const float4 z0 = __ldg(zr + r8 / 4), z1 = __ldg(zr + r8 / 4 + 1);
                 const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-                for (int j = h; j < h + 16; ++j) {
-                  if (j < cols) {
-                    float w[8];
-                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(up + static_cast<int64_t>(j) * p.R + r8)), w);
+                for (int j = h; j < h + 8; ++j) {
+                  float w[8];
+                  unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(up + static_cast<int64_t>(j) * p.R + r8)), w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[j] = fmaf(zz[e], w[e], f[j]);
-                  }
+                  for (int e = 0; e < 8; ++e) f[j] = fmaf(zz[e], w[e], f[j]);
                 }
               }
             }
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row) * p.K + n0 + c0);
+        // through shared memory, so that a warp stores 8 rows of 64 bytes at once
+        __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (8 * q >= cols) break;
-          if (p.bias != nullptr) {
-            const float4* bs = reinterpret_cast<const float4*>(p.bias + n0 + c0 + 8 * q);
-            const float4 b0 = __ldg(bs), b1 = __ldg(bs + 1);
-            f[8 * q] += b0.x;
-            f[8 * q + 1] += b0.y;
-            f[8 * q + 2] += b0.z;
-            f[8 * q + 3] += b0.w;
-            f[8 * q + 4] += b1.x;
-            f[8 * q + 5] += b1.y;
-            f[8 * q + 6] += b1.z;
-            f[8 * q + 7] += b1.w;
-          }
-          dst[q] = pack8<BF16>(f + 8 * q);
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + lane * 80 + 16 * q) = pack8<BF16>(f + 8 * q);
+        __syncwarp();
+        uint8_t* dst = static_cast<uint8_t*>(p.Y) + (static_cast<int64_t>(rt * p.tm + quarter * 32) * p.K + n0 + c0) * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), ch = lane & 3;
+          if (rr < rows && ch * 8 < cols)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(rr) * p.K * 2 + ch * 16) =
+                *reinterpret_cast<const uint4*>(stg + rr * 80 + ch * 16);
         }
       }
-      __syncwarp();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);

@@ -244,16 +244,17 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
     // ------------------------------ TMA producer ------------------------------
     const uint32_t bytes = PAIR ? 2 * (C::A_BYTES + 128 * 128) : C::A_BYTES + 2 * hn * 128;
     const uint32_t lfull = PAIR ? cluster_addr(bfull, 0) : bfull;
-    RingPos at;
+    RingWalk ring(bempty, S::STAGES, 1);
     uint32_t c = 0;
     bool live = true;
     for (int u = u0; u < tiles && live; u += ustep) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
       for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
-        live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+        uint32_t st;
+        live = ring.take(st, kSiteKEmpty, abort_flag);
         if (!live) break;
-        const uint32_t s = sbase + at.st * S::STAGE, bar = lfull + 8 * at.st;
-        if (rank == 0) expect_tx_elect(bfull + 8 * at.st, bytes);
+        const uint32_t s = sbase + st * S::STAGE, bar = lfull + 8 * st;
+        if (rank == 0) expect_tx_elect(bfull + 8 * st, bytes);
         if constexpr (PAIR) {
           load_elect_pair(s, &tmX, ks * C::BK, rt * TROWS + rank * 128, 0, bar);
           load_elect_pair(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, rank, bar);
@@ -262,7 +263,6 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
           load_elect(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, bar);
           load_elect(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, bar);
         }
-        at.next(S::STAGES);
       }
     }
     // every load lands before the CTA (or its pair) can exit
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc = idesc_f16(TROWS, 2 * hn, BF16, false, false);
     const uint64_t adesc = sdesc_sw128(sbase, 16, 1024), bdesc = sdesc_sw128(sbase + C::A_BYTES, 16, 1024);
-    RingPos at;
+    RingWalk ring(bfull, S::STAGES, 0);
     uint32_t ui = 0;
     bool live = true;
     for (int u = u0; u < tiles && live; u += ustep, ++ui) {
@@ -294,23 +294,23 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
       const int turn = chains == 1 ? p.ksteps : (p.ksteps + 1) / 2;
       uint32_t d = tmem + (chains == 1 ? ab * 256 : 0), acc = 0;
       for (int ks = 0; ks < p.ksteps; ++ks) {
-        live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
+        uint32_t st;
+        live = ring.take(st, kSiteKFull, abort_flag);
         if (!live) break;
         tc_fence_after();
         if (BWD && ks == turn) {
           d = tmem + 256;
           acc = 0;
         }
-        const uint64_t off = at.st * (S::STAGE >> 4);
+        const uint64_t off = st * (S::STAGE >> 4);
         if constexpr (PAIR) {
           mma_ss4_pair(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
-          mma_commit_pair(bempty + 8 * at.st);
+          mma_commit_pair(bempty + 8 * st);
         } else {
           mma_ss4(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
-          mma_commit_at(bempty + 8 * at.st);
+          mma_commit_at(bempty + 8 * st);
         }
         acc = 1;
-        at.next(S::STAGES);
       }
       if (live) {
         if constexpr (PAIR) {
@@ -604,18 +604,19 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
     const uint32_t lfull = cluster_addr(bfull, 0);
-    RingPos at;
+    RingWalk ring(bempty, C::STAGES, 1);
     uint32_t c = 0;
     bool live = true;
     for (int u = u0; u < units && live; u += ustep) {
       const ProductUnit t = product_unit(p, u);
       const int slabs = (t.half + 63) / 64, m = t.m0 + rank * 128, n = t.n0 + rank * t.half;
       for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
-        live = wait_warp(bempty + 8 * at.st, at.use ^ 1, kSiteKEmpty, abort_flag);
+        uint32_t st;
+        live = ring.take(st, kSiteKEmpty, abort_flag);
         if (!live) break;
-        const uint32_t s = sbase + at.st * C::STAGE, bar = lfull + 8 * at.st;
+        const uint32_t s = sbase + st * C::STAGE, bar = lfull + 8 * st;
         const int k = ks * C::BK;
-        if (rank == 0) expect_tx_elect(bfull + 8 * at.st, 2 * (C::A_BYTES + slabs * C::SLAB));
+        if (rank == 0) expect_tx_elect(bfull + 8 * st, 2 * (C::A_BYTES + slabs * C::SLAB));
         if (t.side == 0) {
           load_elect_pair(s, &tmPk, k, m, 0, bar);
           load_elect_pair(s + C::A_BYTES, &tmW, n, k, 0, bar);
@@ -626,7 +627,6 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
           load_elect_pair(s + C::A_BYTES, &tmX, n, k, 0, bar);
           if (slabs > 1) load_elect_pair(s + C::A_BYTES + C::SLAB, &tmX, n + 64, k, 0, bar);
         }
-        at.next(C::STAGES);
       }
     }
     if (rank == 0) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
-    RingPos at;
+    RingWalk ring(bfull, C::STAGES, 0);
     uint32_t ui = 0;
     bool live = true;
     for (int u = u0; u < units && live; u += ustep, ++ui) {
@@ -653,14 +653,14 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
       tc_fence_after();
       uint32_t acc = 0;
       for (int ks = t.k0; ks < t.k1; ++ks) {
-        live = wait_warp(bfull + 8 * at.st, at.use, kSiteKFull, abort_flag);
+        uint32_t st;
+        live = ring.take(st, kSiteKFull, abort_flag);
         if (!live) break;
         tc_fence_after();
-        const uint64_t off = at.st * (C::STAGE >> 4);
+        const uint64_t off = st * (C::STAGE >> 4);
         mma_ss4_pair(tmem + ab * 256, adesc + off, bdesc + off, idesc, acc, astep, 128);
-        mma_commit_pair(bempty + 8 * at.st);
+        mma_commit_pair(bempty + 8 * st);
         acc = 1;
-        at.next(C::STAGES);
       }
       if (live) mma_commit_pair(bacc_full + 8 * ab);
     }

@@ -6,9 +6,9 @@
 // issues loads and another products, so what bounds narrow tiles is the code
 // those warps run per step: with every wait's slow path inlined, descriptors
 // built for each MMA and the ring's stage found by division, a step took 480 to
-// 1030 clocks whatever its width.  So here a wait is one try and a call, the
-// four MMAs of a step are one asm block that advances its descriptors, and
-// stages are counted.  The warps stay converged (elect.sync picks the issuing
+// 1030 clocks whatever its width.  So here a wait is one try and a call,
+// the four MMAs of a step are one asm block that advances its
+// descriptors, and stages are counted.  The warps stay converged (elect.sync picks the issuing
 // lane), which keeps operands in uniform registers.
 //
 // Waits have sm100.cuh's limits: a second, then the error word and the CTA's
@@ -19,13 +19,17 @@
 
 namespace sdattn {
 
+// The clock is read only after a good many tries: a read of it costs more than
+// most waits last.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t site, volatile uint32_t* abort_flag) {
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 0u) {
+    if ((it & 127u) == 0u) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
         *abort_flag = 1u;
         atomicCAS(&g_error_word, 0u, 0x100u + site);
         return false;
@@ -41,14 +45,21 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_
   return __all_sync(0xffffffffu, wait_slow(bar, parity, site, abort_flag));
 }
 
-// A stage of a ring of `n` and the parity of its current use.
-struct RingPos {
-  uint32_t st = 0, use = 0;
-  __device__ __forceinline__ void next(uint32_t n) {
+// One warp's walk around a ring of n stages with a barrier each: take() waits
+// for the next stage.  `parity`: 0 for the consumer of full stages, 1 for the
+// producer, whose first turn finds them empty.
+struct RingWalk {
+  uint32_t bars, n, st, parity;
+  __device__ __forceinline__ RingWalk(uint32_t bars_, uint32_t n_, uint32_t parity_)
+      : bars(bars_), n(n_), st(0), parity(parity_) {}
+  __device__ __forceinline__ bool take(uint32_t& stage, uint32_t site, volatile uint32_t* abort_flag) {
+    const bool ok = wait_warp(bars + 8 * st, parity, site, abort_flag);
+    stage = st;
     if (++st == n) {
       st = 0;
-      use ^= 1u;
+      parity ^= 1u;
     }
+    return ok;
   }
 };
 

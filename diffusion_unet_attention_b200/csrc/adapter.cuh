@@ -28,8 +28,9 @@
 // Few rows with an adapter each (the time embedding's projection, single
 // tokens) would cost a phase for every few rows.  There the adapters are
 // per-row work, bound by reading D and U once for each row: adapter_z_kernel
-// computes z with plain fp32 sums (a warp per row and two ranks), and the
-// projection's epilogue adds z U^T, 8 ranks of 32 columns at a time (ROWS).
+// computes z with plain fp32 sums (a warp per row and two ranks); in the
+// projection's kernel the epilogue's warps compute z U^T while the products
+// run (a thread per row and two columns) and leave it in shared memory.
 #pragma once
 
 #include "pipeline.cuh"
@@ -37,13 +38,17 @@
 
 namespace sdattn {
 
+enum : int { kAdapterNone = 0, kAdapterRows = 1, kAdapterMma = 2 };
+
 struct AdapterCfg {
   static constexpr int BK = 64;
   static constexpr int BN = 192;                    // most columns per tile
+  static constexpr int BN_ROWS = 64;                // with per-row adapters
   static constexpr int ZN = 64;                     // ranks per phase
-  static constexpr int RING = 200704;               // bytes of the ring of stages
-  static constexpr int SLACK = 16384;               // kept behind it when x's tiles are short: their products read up to 16 KB past a stage
-  static constexpr int MAX_STAGES = 20;
+  static constexpr int MAX_STAGES = 12;
+  static constexpr int SLACK = 16384;               // kept behind the stages when x's tile is short: its products read up to 16 KB
+  static constexpr int RING = 200704;               // bytes of the ring of stages, and with per-row adapters of z U^T behind it
+  static constexpr int CORR = 128 * (BN_ROWS + 4) * 4;
   static constexpr int OFF_PLAN = RING;
   static constexpr int PLANS = 4;                   // tiles the planner may run ahead
   static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' places, rows' scales, count
@@ -56,6 +61,10 @@ struct AdapterCfg {
   static constexpr int NTHREADS = 512;              // TMA, MMA, planner, idle, eight epilogue warps, four that convert z
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int TM_Z = 2 * BN;               // accumulators at 0 and BN, z at 384 and 448
+  // Contraction steps of 64 per stage: two without tensor-core adapters (half
+  // the waits per step), one with them (their stages are larger).
+  __host__ __device__ static constexpr int sub(int mode) { return mode == kAdapterMma ? 1 : 2; }
+  __host__ __device__ static constexpr int ring(int mode) { return mode == kAdapterRows ? RING - CORR : RING; }
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -73,7 +82,7 @@ struct AdapterParams {
   int ksteps;             // ceil(C / 64)
   int rc;                 // ranks per slot: 16, 32, 48 or 64
   int chunks;             // slots per adapter: ceil(R / 64)
-  int stages, stage;      // of the ring: how many, bytes of one (x, then W or U, then D)
+  int stages, stage;      // of the ring: how many, bytes of one (each step: x, then W or U, then D)
 };
 
 // z[t][r] = s_i x[t] . D_i[r], one warp per row and pair of ranks.
@@ -126,12 +135,46 @@ struct AdapterPlan {
 };
 static_assert(sizeof(AdapterPlan) == AdapterCfg::PLAN, "plan layout");
 
-template <bool BF16, bool ROWS>
+// z U^T of the tile's rows and columns into corr, by the 384 threads of warps
+// 4..15: a thread takes a row and two columns at a time.  Rows without an
+// adapter get zeros.
+template <bool BF16>
+__device__ __forceinline__ void adapter_corr(const AdapterParams& p, float* corr, int row0, int n0) {
+  const int pairs = p.bn / 2, rows = min(p.tm, p.T - row0);
+  for (int i = threadIdx.x - 128; i < rows * pairs; i += 384) {
+    const int r = i / pairs, c = (i - r * pairs) * 2, row = row0 + r, n = n0 + c;
+    float a = 0.f, b = 0.f;
+    const int id = __ldg(p.ids + row / p.rows);
+    if (id >= 0 && id < p.L && n < p.K) {
+      const float4* z = reinterpret_cast<const float4*>(p.z + static_cast<int64_t>(row) * p.R);
+      const uint4* u0 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.U) + (static_cast<int64_t>(id) * p.K + n) * p.R);
+      const uint4* u1 = u0 + p.R / 8;
+#pragma unroll 4
+      for (int q = 0; q < p.R / 8; ++q) {
+        const float4 z0 = __ldg(z + 2 * q), z1 = __ldg(z + 2 * q + 1);
+        const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+        float w0[8], w1[8];
+        unpack8<BF16>(__ldg(u0 + q), w0);
+        unpack8<BF16>(__ldg(u1 + q), w1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a = fmaf(zz[e], w0[e], a);
+          b = fmaf(zz[e], w1[e], b);
+        }
+      }
+    }
+    *reinterpret_cast<float2*>(corr + r * (p.bn + 4) + c) = make_float2(a, b);
+  }
+}
+
+template <bool BF16, int MODE>
 __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     adapter_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
                    const AdapterParams p) {
   using C = AdapterCfg;
+  constexpr bool MMA = MODE == kAdapterMma, ROWS = MODE == kAdapterRows;
+  constexpr int SUB = C::sub(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -147,13 +190,14 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile uint32_t* abort_flag = misc + 1;
   AdapterPlan* plans = reinterpret_cast<AdapterPlan*>(smem + C::OFF_PLAN);
+  float* corr = reinterpret_cast<float*>(smem + C::ring(MODE));   // ROWS: [128][bn + 4], z U^T of the tile
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int tiles = p.rts * p.nts;
   const int spp = C::ZN / p.rc;               // slots per phase
-  const bool planned = !ROWS && p.ids != nullptr;
   const uint32_t NS = p.stages;
   const uint32_t sbase = smem_u32(smem), bfull = smem_u32(full), bempty = smem_u32(empty);
   const int off_w = p.tm * 128, off_d = off_w + p.bn * 128;
+  const int sub = off_d + (MMA ? C::ZN * 128 : 0);   // bytes of a step
   const int mid = p.ksteps / 2;               // the step of x's products after which the last phase's z U^T goes
 
   if (threadIdx.x == 0) {
@@ -178,7 +222,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
-    if (planned) {
+    if (MMA) {
       tma_prefetch_desc(&tmD);
       tma_prefetch_desc(&tmU);
     }
@@ -201,7 +245,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   if (warp == 2) {
     // ------------------------------ planner -----------------------------------
     uint32_t ui = 0;
-    for (int u = blockIdx.x; planned && u < tiles; u += gridDim.x, ++ui) {
+    for (int u = blockIdx.x; MMA && u < tiles; u += gridDim.x, ++ui) {
       const uint32_t pb = ui % C::PLANS, n = ui / C::PLANS;
       if (!wait_warp(smem_u32(&plan_empty[pb]), (n & 1) ^ 1, kSiteTicket, abort_flag)) break;
       AdapterPlan* pl = &plans[pb];
@@ -246,30 +290,35 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_n0 = 0;
     uint32_t pend_pb = 0;
-    for (int u = blockIdx.x; live; u += gridDim.x, ++ui) {
-      const bool more = u < tiles;              // one turn past the last tile: its last phase's U tiles
-      if (!more && !pend) break;
+    for (int u = blockIdx.x; live && (MMA || u < tiles); u += gridDim.x, ++ui) {
+      const bool more = !MMA || u < tiles;      // one turn past the last tile: its last phase's U tiles
+      if (MMA && u >= tiles && !pend) break;
       const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
       const uint32_t pb = ui % C::PLANS;
       int count = 0;
-      if (more && planned) {
+      if (MMA && more) {
         live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
         if (!live) break;
         count = plans[pb].count;
       }
-      const int nph = more ? phases(count) : 1, steps = more ? p.ksteps : 1;
+      const int nph = MMA && more ? phases(count) : 1, steps = more ? p.ksteps : 1;
       for (int ph = 0; ph < nph && live; ++ph) {
-        const int ns = more ? slots_of(count, ph) : 0;
+        const int ns = MMA && more ? slots_of(count, ph) : 0;
         const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + ns * p.rc * 128;
-        for (int ks = 0; ks < steps; ++ks) {
+        for (int ks = 0; ks < steps; ks += SUB) {
           if (more) {
             uint32_t st;
             live = ring.take(st, kSiteKEmpty, abort_flag);
             if (!live) break;
             const uint32_t s = sbase + st * p.stage, bar = bfull + 8 * st;
-            expect_tx_elect(bar, bytes);
+            const bool two = SUB == 2 && ks + 1 < steps;
+            expect_tx_elect(bar, two ? 2 * bytes : bytes);
             load_elect(s, &tmX, ks * C::BK, rt * p.tm, 0, bar);
             if (ph == 0) load_elect(s + off_w, &tmW, ks * C::BK, n0, 0, bar);
+            if (two) {
+              load_elect(s + sub, &tmX, (ks + 1) * C::BK, rt * p.tm, 0, bar);
+              load_elect(s + sub + off_w, &tmW, (ks + 1) * C::BK, n0, 0, bar);
+            }
             for (int j = 0; j < ns; ++j) {
               const int sl = ph * spp + j;
               load_elect(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
@@ -277,7 +326,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             }
             ++c;
           }
-          if (pend && (ks == mid || !more)) {
+          if (MMA && pend && (ks == mid || !more)) {
             // the U tiles of the last phase, one stage per slot
             const AdapterPlan* pl = &plans[pend_pb];
             const int nu = slots_of(pl->count, pend_ph);
@@ -302,7 +351,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           pend_n0 = n0;
           pend_pb = pb;
           pend_last = ph == nph - 1;
-        } else if (more && planned) {
+        } else if (MMA && more) {
           arrive_elect(smem_u32(&plan_empty[pb]));   // a tile without adapters
         }
       }
@@ -324,13 +373,13 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_count = 0;
     uint32_t pend_pb = 0, pend_ab = 0, pend_z = 0;
-    for (int u = blockIdx.x; live; u += gridDim.x, ++ui) {
-      const bool more = u < tiles;              // as in the producer
-      if (!more && !pend) break;
+    for (int u = blockIdx.x; live && (MMA || u < tiles); u += gridDim.x, ++ui) {
+      const bool more = !MMA || u < tiles;      // as in the producer
+      if (MMA && u >= tiles && !pend) break;
       const uint32_t ab = ui & 1, na = ui >> 1, pb = ui % C::PLANS;
       int count = 0;
       if (more) {
-        if (planned) {
+        if (MMA) {
           live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
           if (!live) break;
           count = plans[pb].count;
@@ -339,12 +388,12 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         if (!live) break;
         tc_fence_after();
       }
-      const int nph = more ? phases(count) : 1, steps = more ? p.ksteps : 1;
+      const int nph = MMA && more ? phases(count) : 1, steps = more ? p.ksteps : 1;
       for (int ph = 0; ph < nph && live; ++ph) {
-        const int ns = more ? slots_of(count, ph) : 0;
+        const int ns = MMA && more ? slots_of(count, ph) : 0;
         const uint32_t zb = zc & 1;
         const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
-        for (int ks = 0; ks < steps; ++ks) {
+        for (int ks = 0; ks < steps; ks += SUB) {
           if (more) {
             uint32_t st;
             live = ring.take(st, kSiteKFull, abort_flag);
@@ -352,10 +401,14 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             tc_fence_after();
             const uint64_t off = st * (p.stage >> 4);
             if (ph == 0) mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
+            if (SUB == 2 && ks + 1 < steps) {
+              const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
+              mma_ss4(tmem + ab * C::BN, xdesc + off2, wdesc + off2, idesc_w, 1, 2, 2);
+            }
             if (ns > 0) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
             mma_commit_at(bempty + 8 * st);
           }
-          if (pend && (ks == mid || !more)) {
+          if (MMA && pend && (ks == mid || !more)) {
             // z U^T of the last phase onto its tile's accumulator
             const uint32_t pz = pend_z & 1;
             live = wait_warp(smem_u32(&p_full[pz]), (pend_z >> 1) & 1, kSitePFull, abort_flag);
@@ -394,7 +447,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           pend_last = ph == nph - 1;
         } else {
           mma_commit_at(smem_u32(&acc_full[ab]));
-          if (planned) arrive_elect(smem_u32(&plan_empty[pb]));
+          if (MMA) arrive_elect(smem_u32(&plan_empty[pb]));
         }
       }
       if (!more) break;
@@ -402,13 +455,21 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     volatile uint32_t never = 0;
     mma_commit_at(smem_u32(drain_bar));
     wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
-  } else if (warp >= 12) {
+  } else if (ROWS && warp >= 12) {
+    // ------------------------------ z U^T -------------------------------------
+    for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
+      const int rt = u / p.nts;
+      adapter_corr<BF16>(p, corr, rt * p.tm, (u - rt * p.nts) * p.bn);
+      named_bar_sync(1, 384);                   // z U^T is complete
+      named_bar_sync(2, 384);                   // and has been read
+    }
+  } else if (MMA && warp >= 12) {
     // ------------------------------ conversion of z ---------------------------
     const int quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int r = quarter * 32 + lane;
     uint32_t ui = 0, zc = 0;
-    bool live = planned;
+    bool live = MMA;
     for (int u = blockIdx.x; u < tiles && live; u += gridDim.x, ++ui) {
       const uint32_t pb = ui % C::PLANS;
       live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
@@ -451,7 +512,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         if (lane == 0) mbar_arrive(&p_full[zb]);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------ epilogue ----------------------------------
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -468,18 +529,19 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const int n = n0 + c0 + lane;
         sb[i] = p.bias != nullptr && n < p.K ? __ldg(p.bias + n) : 0.f;
       }
-      int id = -1;                              // ROWS: this row's adapter
-      if (ROWS && lane < rows) {
-        id = __ldg(p.ids + row / p.rows);
-        if (id >= p.L) id = -1;
+      if constexpr (ROWS) {
+        adapter_corr<BF16>(p, corr, rt * p.tm, n0);
+        named_bar_sync(1, 384);
       }
       __syncwarp();
-      if (!wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag)) break;
+      const bool live = wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag);
+      // a CTA that gives up keeps its barriers' company to the last tile
+      if (!live && !ROWS) break;
       tc_fence_after();
       // 32 columns at a time (the last ones 16), the two warps of a quarter in turn
       const float* bs = sb;
 #pragma unroll 1
-      for (int c0 = half * 32; c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 64, bs += 32) {
+      for (int c0 = half * 32; live && c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 64, bs += 32) {
         uint32_t v[32];
         tmem_ld_x32(tmem + ab * C::BN + c0 + lane_off, v);
         tmem_wait_ld();
@@ -495,22 +557,15 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           f[4 * q + 3] = __uint_as_float(v[4 * q + 3]) + b.w;
         }
         if constexpr (ROWS) {
-          if (id >= 0) {
-            const float4* zr = reinterpret_cast<const float4*>(p.z + static_cast<int64_t>(row) * p.R);
-            const uint16_t* up = static_cast<const uint16_t*>(p.U) + (static_cast<int64_t>(id) * p.K + n0 + c0) * p.R;
+          const float4* cr = reinterpret_cast<const float4*>(corr + r * (p.bn + 4) + c0);
 #pragma unroll
-            for (int h = 0; h < 32; h += 8) {     // 8 columns' U in flight
-              for (int r8 = 0; r8 < p.R && h < cols; r8 += 8) {
-                const float4 z0 = __ldg(zr + r8 / 4), z1 = __ldg(zr + r8 / 4 + 1);
-                const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-#pragma unroll
-                for (int j = h; j < h + 8; ++j) {
-                  float w[8];
-                  unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(up + static_cast<int64_t>(j) * p.R + r8)), w);
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) f[j] = fmaf(zz[e], w[e], f[j]);
-                }
-              }
+          for (int q = 0; q < 8; ++q) {
+            if (4 * q < cols) {
+              const float4 b = cr[q];
+              f[4 * q] += b.x;
+              f[4 * q + 1] += b.y;
+              f[4 * q + 2] += b.z;
+              f[4 * q + 3] += b.w;
             }
           }
         }
@@ -528,6 +583,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
                 *reinterpret_cast<const uint4*>(stg + rr * 80 + ch * 16);
         }
       }
+      if constexpr (ROWS) named_bar_sync(2, 384);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);

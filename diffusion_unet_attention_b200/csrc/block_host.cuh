@@ -177,8 +177,8 @@ CUtensorMapDataType elem16(int dtype) {
 // Pairs of CTAs on tiles of 256 rows by 128 columns of h, or single CTAs on
 // 128 rows by hn columns (a multiple of 16 up to 128): the fewest waves of the
 // longest of a tile's products (2 clocks per accumulator column and 64 of C),
-// loads (45 bytes per clock and SM, measured with the epilogue left out) and
-// epilogue, plus one tile's epilogue at the end.  Many rows take pairs, which
+// issue (300 clocks a step), loads (45 bytes per clock and SM, measured with the
+// epilogue left out) and epilogue, plus one tile's epilogue at the end.  Many rows take pairs, which
 // read W's tile once for 256 rows; few rows narrower tiles, until there is
 // about one per SM.
 struct GatedPlan {
@@ -191,7 +191,7 @@ GatedPlan plan_gated(const sdattn_ff_desc* d, bool backward, int nsm) {
   const double epi = backward ? 40.0 : 20.0;      // clocks per column of a 128-row tile
   auto cost = [&](int64_t tiles, int64_t slots, int hn, double bytes) {
     const double waves = static_cast<double>((tiles + slots - 1) / slots);
-    return waves * std::max(ksteps * std::max(4.0 * hn, bytes / 45.0), epi * hn) + epi * hn;
+    return waves * std::max(ksteps * std::max(std::max(4.0 * hn, 300.0), bytes / 45.0), epi * hn) + epi * hn;
   };
   GatedPlan best{true, 128};
   double least = 1e300;
@@ -226,6 +226,10 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   p.rts = static_cast<int>(plan.pair ? (T + 255) / 256 : (T + 127) / 128);
   p.fts = (d->F + p.hn - 1) / p.hn;
   p.ksteps = (d->C + 63) / 64;
+  p.tm = plan.pair ? 128 : static_cast<int>(std::min<uint64_t>(128, (T + 7) / 8 * 8));
+  using Smem = sdattn::GatedSmem<BWD, false>;
+  p.stage = 2 * (p.tm + 2 * p.hn) * 128;
+  p.stages = std::min(Smem::MAX_STAGES, (Smem::RING - (p.tm < 128 ? Smem::SLACK : 0)) / p.stage);
   // The tensor cores' fp32 sums truncate: an entry of h or g comes out low by
   // about 1.2e-9 of its terms per column of C, which all rows share and db
   // adds up (1.5e-6 of db at C = 1280).  Past C = 640 the backward pass halves
@@ -233,7 +237,7 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   p.chains = BWD && p.ksteps > 10 ? 2 : 1;
   const CUtensorMapDataType dt = elem16(d->dtype);
   CUtensorMap mx, mw, my;
-  if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, 128)) return SDATTN_ERR_CUDA;
+  if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, F, 2, C * 2, F * C * 2, 64, static_cast<uint32_t>(p.hn))) return SDATTN_ERR_CUDA;
   const uint64_t ldy = BWD ? 4 * F : 2 * F;   // bytes of a row of y, or of P = [dh, dg]
   if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, BWD ? 32 : 64, 32,
@@ -385,20 +389,20 @@ size_t adapter_ws_bytes(const sdattn_adapter_desc* d) {
   return adapter_rows(d) ? static_cast<size_t>(d->T) * d->R * sizeof(float) : 0;
 }
 
-// Columns per tile (a multiple of 16 up to 192): the fewest waves of the
-// longer of a tile's products (2 clocks per column and 64 of C, the adapters'
-// ranks included) and loads (45 bytes per clock and SM), its epilogue beside
-// them, plus one epilogue at the end.
-int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int nsm) {
+// Columns per tile (a multiple of 16 up to `most`): the fewest waves of the
+// longest of a tile's products (2 clocks per column and 64 of C, the adapters'
+// ranks included), issue (300 clocks a step), loads (45 bytes per clock and SM)
+// and epilogue, plus one epilogue at the end.
+int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int most, int nsm) {
   const int64_t rts = (d->T + tm - 1) / tm;
   const double ksteps = (d->C + 63) / 64;
-  int best_bn = sdattn::AdapterCfg::BN;
+  int best_bn = most;
   double best = 1e300;
-  for (int bn = sdattn::AdapterCfg::BN; bn >= 16; bn -= 16) {
+  for (int bn = most; bn >= 16; bn -= 16) {
     const int64_t tiles = rts * ((d->K + bn - 1) / bn);
     const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
-    const double tile = std::max(ksteps * std::max(2.0 * (bn + rc), 128.0 * (tm + bn + rc) / 45.0), 8.0 * bn);
-    const double cost = waves * tile + 8.0 * bn;
+    const double step = std::max(std::max(2.0 * (bn + rc), 300.0), 128.0 * (tm + bn + rc) / 45.0);
+    const double cost = waves * std::max(ksteps * step, 12.0 * bn) + 12.0 * bn;
     if (cost < best) {
       best = cost;
       best_bn = bn;
@@ -407,11 +411,12 @@ int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int nsm) {
   return best_bn;
 }
 
-template <bool BF16, bool ROWS>
+template <bool BF16, int MODE>
 sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const void* W, const float* bias,
                              const void* D, const void* U, const float* scale, const int32_t* ids, void* Y, void* ws,
                              cudaStream_t s) {
   using Cfg = sdattn::AdapterCfg;
+  constexpr bool MMA = MODE == sdattn::kAdapterMma, ROWS = MODE == sdattn::kAdapterRows;
   const int dev = current_device();
   if (dev < 0) return SDATTN_ERR_CUDA;
   const int nsm = sm_count(dev);
@@ -425,24 +430,23 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.Y = Y;
   p.T = static_cast<int>(T);
   p.K = d->K;
-  p.L = ids ? d->L : 0;
+  p.L = d->L;
   p.R = d->R;
   p.rows = d->rows;
-  const bool mma = ids && !ROWS;                    // adapters on the tensor cores
   p.rc = std::max(16, std::min(64, (d->R + 15) / 16 * 16));
   p.chunks = std::max(1, (d->R + 63) / 64);
   p.tm = static_cast<int>(std::min<uint64_t>(128, (T + 7) / 8 * 8));
-  p.bn = plan_adapter(d, p.tm, mma ? p.rc : 0, nsm);
+  p.bn = plan_adapter(d, p.tm, MMA ? p.rc : 0, ROWS ? Cfg::BN_ROWS : Cfg::BN, nsm);
   p.rts = static_cast<int>((T + p.tm - 1) / p.tm);
   p.nts = (d->K + p.bn - 1) / p.bn;
   p.ksteps = (d->C + 63) / 64;
-  p.stage = p.tm * 128 + p.bn * 128 + (mma ? Cfg::ZN * 128 : 0);
-  p.stages = std::min(Cfg::MAX_STAGES, (Cfg::RING - (p.tm < 128 ? Cfg::SLACK : 0)) / p.stage);
+  p.stage = Cfg::sub(MODE) * (p.tm * 128 + p.bn * 128 + (MMA ? Cfg::ZN * 128 : 0));
+  p.stages = std::min(Cfg::MAX_STAGES, (Cfg::ring(MODE) - (p.tm < 128 ? Cfg::SLACK : 0)) / p.stage);
   const CUtensorMapDataType dt = elem16(d->dtype);
   CUtensorMap mx, mw, md, mu;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, K, 1, C * 2, K * C * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
-  if (mma) {
+  if (MMA) {
     if (!make_map_3d(&md, D, dt, C, R, L, C * 2, R * C * 2, 64, static_cast<uint32_t>(p.rc))) return SDATTN_ERR_CUDA;
     if (!make_map_3d(&mu, U, dt, R, K, L, R * 2, K * R * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
   } else {
@@ -455,9 +459,18 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
                 p.T, d->C, d->L, d->R, d->rows))
       return SDATTN_ERR_CUDA;
   }
-  auto kern = sdattn::adapter_kernel<BF16, ROWS>;
+  auto kern = sdattn::adapter_kernel<BF16, MODE>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, Cfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.nts));
   return launch(kern, grid, Cfg::NTHREADS, Cfg::SMEM, s, mx, mw, md, mu, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+}
+
+template <bool BF16>
+sdattn_status dispatch_adapter(const sdattn_adapter_desc* d, const void* X, const void* W, const float* bias,
+                               const void* D, const void* U, const float* scale, const int32_t* ids, void* Y, void* ws,
+                               cudaStream_t s) {
+  if (!ids) return launch_adapter<BF16, sdattn::kAdapterNone>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
+  if (adapter_rows(d)) return launch_adapter<BF16, sdattn::kAdapterRows>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
+  return launch_adapter<BF16, sdattn::kAdapterMma>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
 }

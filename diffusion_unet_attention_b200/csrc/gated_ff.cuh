@@ -106,17 +106,22 @@ struct GatedCfg {
   static constexpr uint32_t TMEM_COLS = 512;        // two accumulators of 2 HN columns
 };
 
-// PAIR: a CTA holds its 128 rows of x and the h or the g half of W's tile.
+// PAIR: a stage is 64 columns of C of the CTA's 128 rows of x and the h or the
+// g half of W's tile.  Otherwise it is 128 columns (two halves) of tm rows of x
+// and hn rows each of Wh and Wg, as many as the ring holds.
 template <bool BWD, bool PAIR>
 struct GatedSmem {
-  static constexpr int STAGE = GatedCfg::A_BYTES + (PAIR ? 1 : 2) * GatedCfg::HN * 128;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGE = 2 * 128 * 128;       // PAIR
+  static constexpr int STAGES = 4;                  // PAIR
+  static constexpr int RING = PAIR ? STAGES * STAGE : 212992;
+  static constexpr int SLACK = 16384;               // kept behind the stages when x's tile is short: its products read up to 16 KB
+  static constexpr int MAX_STAGES = 12;
   // an epilogue warp's staged output (PAIR): 32 rows x 64 columns of y, or x 32 of dh and of dg
   static constexpr int WSTG = PAIR ? 4096 : 0;
-  static constexpr int OFF_STG = STAGES * STAGE;
+  static constexpr int OFF_STG = RING;
   static constexpr int OFF_BIAS = OFF_STG + 2 * GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
   static constexpr int OFF_BAR = OFF_BIAS + 2 * 2 * GatedCfg::HN * 4;
-  static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;
+  static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 1;
   static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory budget");
 };
@@ -128,6 +133,8 @@ struct GatedParams {
   float* part;          // [ceil(T / 32)][2F] partial sums of db, or null
   int T, F;
   int hn;               // columns of h per tile: a multiple of 16, at most 128
+  int tm;               // rows of x loaded per CTA: 128, or all rows of a shorter x rounded up to 8
+  int stages, stage;    // of the ring without pairs: how many, bytes of one
   int rts, fts;         // row tiles (of 256 rows in a pair), column tiles
   int ksteps;           // ceil(C / 64)
   int chains;           // accumulators a tile's contraction is dealt over: 1, or 2 (backward, long contractions)
@@ -183,9 +190,9 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-  uint64_t* full = bars;                     // [STAGES] TMA -> MMA (the leader's; both CTAs' loads)
-  uint64_t* empty = full + S::STAGES;        // [STAGES] MMA -> TMA
-  uint64_t* acc_full = empty + S::STAGES;    // [2] MMA -> epilogue
+  uint64_t* full = bars;                     // [stages] TMA -> MMA (the leader's; both CTAs' loads)
+  uint64_t* empty = full + S::MAX_STAGES;    // [stages] MMA -> TMA
+  uint64_t* acc_full = empty + S::MAX_STAGES;   // [2] MMA -> epilogue
   uint64_t* acc_empty = acc_full + 2;        // [2] epilogue -> MMA (the leader's; both CTAs' warps)
   uint64_t* bias_full = acc_empty + 2;       // [2] bias warp -> epilogue
   uint64_t* bias_empty = bias_full + 2;      // [2] back
@@ -199,9 +206,12 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
   const int u0 = PAIR ? blockIdx.x / 2 : blockIdx.x, ustep = PAIR ? gridDim.x / 2 : gridDim.x;
   constexpr int TROWS = PAIR ? 256 : 128;    // rows per tile
+  constexpr int SUB = PAIR ? 1 : 2;          // contraction steps of 64 per stage
+  const int nstages = PAIR ? S::STAGES : p.stages, stage = PAIR ? S::STAGE : p.stage;
+  const int off_w = PAIR ? C::A_BYTES : p.tm * 128, sub = off_w + (PAIR ? 128 : 2 * hn) * 128;   // bytes of a step
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::STAGES; ++i) {
+    for (int i = 0; i < nstages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -242,42 +252,47 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    const uint32_t bytes = PAIR ? 2 * (C::A_BYTES + 128 * 128) : C::A_BYTES + 2 * hn * 128;
     const uint32_t lfull = PAIR ? cluster_addr(bfull, 0) : bfull;
-    RingWalk ring(bempty, S::STAGES, 1);
+    RingWalk ring(bempty, nstages, 1);
     uint32_t c = 0;
     bool live = true;
     for (int u = u0; u < tiles && live; u += ustep) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
-      for (int ks = 0; ks < p.ksteps; ++ks, ++c) {
+      for (int ks = 0; ks < p.ksteps; ks += SUB, ++c) {
         uint32_t st;
         live = ring.take(st, kSiteKEmpty, abort_flag);
         if (!live) break;
-        const uint32_t s = sbase + st * S::STAGE, bar = lfull + 8 * st;
-        if (rank == 0) expect_tx_elect(bfull + 8 * st, bytes);
+        const uint32_t s = sbase + st * stage, bar = lfull + 8 * st;
+        const bool two = SUB == 2 && ks + 1 < p.ksteps;
+        if (rank == 0) expect_tx_elect(bfull + 8 * st, PAIR ? 2 * S::STAGE : two ? 2 * sub : sub);
         if constexpr (PAIR) {
           load_elect_pair(s, &tmX, ks * C::BK, rt * TROWS + rank * 128, 0, bar);
           load_elect_pair(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, rank, bar);
         } else {
           load_elect(s, &tmX, ks * C::BK, rt * TROWS, 0, bar);
-          load_elect(s + C::A_BYTES, &tmW, ks * C::BK, ft * hn, 0, bar);
-          load_elect(s + C::A_BYTES + hn * 128, &tmW, ks * C::BK, ft * hn, 1, bar);
+          load_elect(s + off_w, &tmW, ks * C::BK, ft * hn, 0, bar);
+          load_elect(s + off_w + hn * 128, &tmW, ks * C::BK, ft * hn, 1, bar);
+          if (two) {
+            load_elect(s + sub, &tmX, (ks + 1) * C::BK, rt * TROWS, 0, bar);
+            load_elect(s + sub + off_w, &tmW, (ks + 1) * C::BK, ft * hn, 0, bar);
+            load_elect(s + sub + off_w + hn * 128, &tmW, (ks + 1) * C::BK, ft * hn, 1, bar);
+          }
         }
       }
     }
     // every load lands before the CTA (or its pair) can exit
     if (rank == 0) {
       volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < S::STAGES && st < c; ++st) {
-        const uint32_t uses = (c - st + S::STAGES - 1) / S::STAGES;
+      for (uint32_t st = 0; st < static_cast<uint32_t>(nstages) && st < c; ++st) {
+        const uint32_t uses = (c - st + nstages - 1) / nstages;
         wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
       }
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc = idesc_f16(TROWS, 2 * hn, BF16, false, false);
-    const uint64_t adesc = sdesc_sw128(sbase, 16, 1024), bdesc = sdesc_sw128(sbase + C::A_BYTES, 16, 1024);
-    RingWalk ring(bfull, S::STAGES, 0);
+    const uint64_t adesc = sdesc_sw128(sbase, 16, 1024), bdesc = sdesc_sw128(sbase + off_w, 16, 1024);
+    RingWalk ring(bfull, nstages, 0);
     uint32_t ui = 0;
     bool live = true;
     for (int u = u0; u < tiles && live; u += ustep, ++ui) {
@@ -291,9 +306,10 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
       }
       if (!live) break;
       tc_fence_after();
-      const int turn = chains == 1 ? p.ksteps : (p.ksteps + 1) / 2;
+      // the step where the second chain begins: a whole stage's first
+      const int turn = chains == 1 ? p.ksteps : (p.ksteps + 3) / 4 * 2;
       uint32_t d = tmem + (chains == 1 ? ab * 256 : 0), acc = 0;
-      for (int ks = 0; ks < p.ksteps; ++ks) {
+      for (int ks = 0; ks < p.ksteps; ks += SUB) {
         uint32_t st;
         live = ring.take(st, kSiteKFull, abort_flag);
         if (!live) break;
@@ -302,12 +318,16 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
           d = tmem + 256;
           acc = 0;
         }
-        const uint64_t off = st * (S::STAGE >> 4);
+        const uint64_t off = st * (static_cast<uint32_t>(stage) >> 4);
         if constexpr (PAIR) {
           mma_ss4_pair(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
           mma_commit_pair(bempty + 8 * st);
         } else {
           mma_ss4(d, adesc + off, bdesc + off, idesc, acc, 2, 2);
+          if (ks + 1 < p.ksteps) {
+            const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
+            mma_ss4(d, adesc + off2, bdesc + off2, idesc, 1, 2, 2);
+          }
           mma_commit_at(bempty + 8 * st);
         }
         acc = 1;

@@ -1214,17 +1214,13 @@ sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void*
   if (!aligned16(X) || !aligned16(W) || !aligned16(bias) || !aligned16(D) || !aligned16(U) || !aligned16(Y) ||
       !aligned_to(scale, 4) || !aligned_to(ids, 4))
     return SDATTN_ERR_ALIGNMENT;
-  const bool rows = ids != nullptr && adapter_rows(desc), bf16 = desc->dtype == SDATTN_BF16;
-  if (rows) {
+  if (ids && adapter_rows(desc)) {
     if (!ws || ws_bytes < adapter_ws_bytes(desc)) return SDATTN_ERR_WORKSPACE;
     if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rows)
-    return bf16 ? launch_adapter<true, true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s)
-                : launch_adapter<false, true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s);
-  return bf16 ? launch_adapter<true, false>(desc, X, W, bias, D, U, scale, ids, Y, nullptr, s)
-              : launch_adapter<false, false>(desc, X, W, bias, D, U, scale, ids, Y, nullptr, s);
+  return desc->dtype == SDATTN_BF16 ? dispatch_adapter<true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s)
+                                    : dispatch_adapter<false>(desc, X, W, bias, D, U, scale, ids, Y, ws, s);
 }
 
 const char* sdattn_status_string(sdattn_status status) {

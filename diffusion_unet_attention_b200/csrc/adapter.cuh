@@ -47,23 +47,22 @@ struct AdapterCfg {
   static constexpr int ZN = 64;                     // ranks per phase
   static constexpr int MAX_STAGES = 12;
   static constexpr int SLACK = 16384;               // kept behind the stages when x's tile is short: its products read up to 16 KB
-  static constexpr int RING = 200704;               // bytes of the ring of stages, and with per-row adapters of z U^T behind it
+  static constexpr int RING = 180224;               // bytes of the ring of stages, and with per-row adapters of z U^T behind it
   static constexpr int CORR = 128 * (BN_ROWS + 4) * 4;
   static constexpr int OFF_PLAN = RING;
-  static constexpr int PLANS = 4;                   // tiles the planner may run ahead
+  static constexpr int PLANS = 3;                   // tiles the planner may run ahead
   static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' places, rows' scales, count
-  static constexpr int OFF_STG = OFF_PLAN + PLANS * PLAN;   // [8 epilogue warps] 32 rows of 32 columns, 80 bytes apart
+  static constexpr int EPI = 16;                    // epilogue warps, four per quarter of a tile's rows
+  static constexpr int OFF_STG = OFF_PLAN + PLANS * PLAN;   // [EPI] 32 rows of 32 columns, 80 bytes apart
   static constexpr int STG = 32 * 80;
-  static constexpr int OFF_BIAS = OFF_STG + 8 * STG;        // [8 epilogue warps] biases of up to 96 columns
-  static constexpr int OFF_BAR = OFF_BIAS + 8 * 96 * 4;
+  static constexpr int OFF_BIAS = OFF_STG + EPI * STG;      // [EPI] biases of up to 64 columns
+  static constexpr int OFF_BAR = OFF_BIAS + EPI * 64 * 4;
   static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 2 * PLANS + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-  static constexpr int NTHREADS = 512;              // TMA, MMA, planner, idle, eight epilogue warps, four that convert z
+  static constexpr int NTHREADS = (8 + EPI) * 32;   // TMA, MMA, planner, idle, epilogue, four that convert z
+  static constexpr int CORR_THREADS = (4 + EPI) * 32;   // that compute z U^T of single rows
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int TM_Z = 2 * BN;               // accumulators at 0 and BN, z at 384 and 448
-  // Contraction steps of 64 per stage: two without tensor-core adapters (half
-  // the waits per step), one with them (their stages are larger).
-  __host__ __device__ static constexpr int sub(int mode) { return mode == kAdapterMma ? 1 : 2; }
   __host__ __device__ static constexpr int ring(int mode) { return mode == kAdapterRows ? RING - CORR : RING; }
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -83,6 +82,7 @@ struct AdapterParams {
   int rc;                 // ranks per slot: 16, 32, 48 or 64
   int chunks;             // slots per adapter: ceil(R / 64)
   int stages, stage;      // of the ring: how many, bytes of one (each step: x, then W or U, then D)
+  int sub;                // contraction steps of 64 per stage: two (half the waits per step) where three such stages fit, else one
 };
 
 // z[t][r] = s_i x[t] . D_i[r], one warp per row and pair of ranks.
@@ -135,13 +135,13 @@ struct AdapterPlan {
 };
 static_assert(sizeof(AdapterPlan) == AdapterCfg::PLAN, "plan layout");
 
-// z U^T of the tile's rows and columns into corr, by the 384 threads of warps
-// 4..15: a thread takes a row and two columns at a time.  Rows without an
+// z U^T of the tile's rows and columns into corr, by the threads of the
+// warps from 4 on: a thread takes a row and two columns at a time.  Rows without an
 // adapter get zeros.
 template <bool BF16>
 __device__ __forceinline__ void adapter_corr(const AdapterParams& p, float* corr, int row0, int n0) {
   const int pairs = p.bn / 2, rows = min(p.tm, p.T - row0);
-  for (int i = threadIdx.x - 128; i < rows * pairs; i += 384) {
+  for (int i = threadIdx.x - 128; i < rows * pairs; i += AdapterCfg::CORR_THREADS) {
     const int r = i / pairs, c = (i - r * pairs) * 2, row = row0 + r, n = n0 + c;
     float a = 0.f, b = 0.f;
     const int id = __ldg(p.ids + row / p.rows);
@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
                    const AdapterParams p) {
   using C = AdapterCfg;
   constexpr bool MMA = MODE == kAdapterMma, ROWS = MODE == kAdapterRows;
-  constexpr int SUB = C::sub(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   const uint32_t sbase = smem_u32(smem), bfull = smem_u32(full), bempty = smem_u32(empty);
   const int off_w = p.tm * 128, off_d = off_w + p.bn * 128;
   const int sub = off_d + (MMA ? C::ZN * 128 : 0);   // bytes of a step
-  const int mid = p.ksteps / 2;               // the step of x's products after which the last phase's z U^T goes
+  const int mid = p.ksteps / 2 / p.sub * p.sub;   // the step of x's products after which the last phase's z U^T goes
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], C::EPI);
       mbar_init(&z_full[i], 1);
       mbar_init(&p_full[i], 4);
     }
@@ -305,24 +304,24 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       for (int ph = 0; ph < nph && live; ++ph) {
         const int ns = MMA && more ? slots_of(count, ph) : 0;
         const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + ns * p.rc * 128;
-        for (int ks = 0; ks < steps; ks += SUB) {
+        for (int ks = 0; ks < steps; ks += p.sub) {
           if (more) {
             uint32_t st;
             live = ring.take(st, kSiteKEmpty, abort_flag);
             if (!live) break;
             const uint32_t s = sbase + st * p.stage, bar = bfull + 8 * st;
-            const bool two = SUB == 2 && ks + 1 < steps;
+            const bool two = p.sub == 2 && ks + 1 < steps;
             expect_tx_elect(bar, two ? 2 * bytes : bytes);
             load_elect(s, &tmX, ks * C::BK, rt * p.tm, 0, bar);
             if (ph == 0) load_elect(s + off_w, &tmW, ks * C::BK, n0, 0, bar);
             if (two) {
               load_elect(s + sub, &tmX, (ks + 1) * C::BK, rt * p.tm, 0, bar);
-              load_elect(s + sub + off_w, &tmW, (ks + 1) * C::BK, n0, 0, bar);
+              if (ph == 0) load_elect(s + sub + off_w, &tmW, (ks + 1) * C::BK, n0, 0, bar);
             }
             for (int j = 0; j < ns; ++j) {
-              const int sl = ph * spp + j;
-              load_elect(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, sl % p.chunks * 64,
-                         plans[pb].adapter[sl / p.chunks], bar);
+              const int sl = ph * spp + j, a = plans[pb].adapter[sl / p.chunks], r0 = sl % p.chunks * 64;
+              load_elect(s + off_d + j * p.rc * 128, &tmD, ks * C::BK, r0, a, bar);
+              if (two) load_elect(s + sub + off_d + j * p.rc * 128, &tmD, (ks + 1) * C::BK, r0, a, bar);
             }
             ++c;
           }
@@ -393,19 +392,23 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         const int ns = MMA && more ? slots_of(count, ph) : 0;
         const uint32_t zb = zc & 1;
         const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
-        for (int ks = 0; ks < steps; ks += SUB) {
+        for (int ks = 0; ks < steps; ks += p.sub) {
           if (more) {
             uint32_t st;
             live = ring.take(st, kSiteKFull, abort_flag);
             if (!live) break;
             tc_fence_after();
             const uint64_t off = st * (p.stage >> 4);
-            if (ph == 0) mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
-            if (SUB == 2 && ks + 1 < steps) {
-              const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
-              mma_ss4(tmem + ab * C::BN, xdesc + off2, wdesc + off2, idesc_w, 1, 2, 2);
+            const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
+            const bool two = p.sub == 2 && ks + 1 < steps;
+            if (ph == 0) {
+              mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
+              if (two) mma_ss4(tmem + ab * C::BN, xdesc + off2, wdesc + off2, idesc_w, 1, 2, 2);
             }
-            if (ns > 0) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
+            if (MMA && ns > 0) {
+              mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
+              if (two) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off2, ddesc + off2, idesc_d, 1, 2, 2);
+            }
             mma_commit_at(bempty + 8 * st);
           }
           if (MMA && pend && (ks == mid || !more)) {
@@ -455,15 +458,15 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     volatile uint32_t never = 0;
     mma_commit_at(smem_u32(drain_bar));
     wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
-  } else if (ROWS && warp >= 12) {
+  } else if (ROWS && warp >= 4 + C::EPI) {
     // ------------------------------ z U^T -------------------------------------
     for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
       const int rt = u / p.nts;
       adapter_corr<BF16>(p, corr, rt * p.tm, (u - rt * p.nts) * p.bn);
-      named_bar_sync(1, 384);                   // z U^T is complete
-      named_bar_sync(2, 384);                   // and has been read
+      named_bar_sync(1, C::CORR_THREADS);                   // z U^T is complete
+      named_bar_sync(2, C::CORR_THREADS);                   // and has been read
     }
-  } else if (MMA && warp >= 12) {
+  } else if (MMA && warp >= 4 + C::EPI) {
     // ------------------------------ conversion of z ---------------------------
     const int quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -512,12 +515,12 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
         if (lane == 0) mbar_arrive(&p_full[zb]);
       }
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + C::EPI) {
     // ------------------------------ epilogue ----------------------------------
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stg = smem + C::OFF_STG + (warp - 4) * C::STG;
-    float* sb = reinterpret_cast<float*>(smem + C::OFF_BIAS) + (warp - 4) * 96;
+    float* sb = reinterpret_cast<float*>(smem + C::OFF_BIAS) + (warp - 4) * 64;
     uint32_t ui = 0;
     for (int u = blockIdx.x; u < tiles; u += gridDim.x, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
@@ -525,23 +528,23 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       const int r = quarter * 32 + lane, row = rt * p.tm + r;
       const int rows = min(min(p.tm - quarter * 32, 32), p.T - rt * p.tm - quarter * 32);   // of this warp
       __syncwarp();
-      for (int c0 = half * 32, i = lane; c0 < p.bn; c0 += 64, i += 32) {
+      for (int c0 = part * 32, i = lane; c0 < p.bn; c0 += 128, i += 32) {
         const int n = n0 + c0 + lane;
         sb[i] = p.bias != nullptr && n < p.K ? __ldg(p.bias + n) : 0.f;
       }
       if constexpr (ROWS) {
         adapter_corr<BF16>(p, corr, rt * p.tm, n0);
-        named_bar_sync(1, 384);
+        named_bar_sync(1, C::CORR_THREADS);
       }
       __syncwarp();
       const bool live = wait_warp(smem_u32(&acc_full[ab]), na & 1, kSiteAccFull, abort_flag);
       // a CTA that gives up keeps its barriers' company to the last tile
       if (!live && !ROWS) break;
       tc_fence_after();
-      // 32 columns at a time (the last ones 16), the two warps of a quarter in turn
+      // 32 columns at a time (the last ones 16), the four warps of a quarter in turn
       const float* bs = sb;
 #pragma unroll 1
-      for (int c0 = half * 32; live && c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 64, bs += 32) {
+      for (int c0 = part * 32; live && c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 128, bs += 32) {
         uint32_t v[32];
         tmem_ld_x32(tmem + ab * C::BN + c0 + lane_off, v);
         tmem_wait_ld();
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
                 *reinterpret_cast<const uint4*>(stg + rr * 80 + ch * 16);
         }
       }
-      if constexpr (ROWS) named_bar_sync(2, 384);
+      if constexpr (ROWS) named_bar_sync(2, C::CORR_THREADS);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);

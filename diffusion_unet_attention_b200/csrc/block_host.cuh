@@ -440,8 +440,11 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.rts = static_cast<int>((T + p.tm - 1) / p.tm);
   p.nts = (d->K + p.bn - 1) / p.bn;
   p.ksteps = (d->C + 63) / 64;
-  p.stage = Cfg::sub(MODE) * (p.tm * 128 + p.bn * 128 + (MMA ? Cfg::ZN * 128 : 0));
-  p.stages = std::min(Cfg::MAX_STAGES, (Cfg::ring(MODE) - (p.tm < 128 ? Cfg::SLACK : 0)) / p.stage);
+  const int step = p.tm * 128 + p.bn * 128 + (MMA ? Cfg::ZN * 128 : 0);
+  const int room = Cfg::ring(MODE) - (p.tm < 128 ? Cfg::SLACK : 0);
+  p.sub = room / (2 * step) >= 3 ? 2 : 1;
+  p.stage = p.sub * step;
+  p.stages = std::min(Cfg::MAX_STAGES, room / p.stage);
   const CUtensorMapDataType dt = elem16(d->dtype);
   CUtensorMap mx, mw, md, mu;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;

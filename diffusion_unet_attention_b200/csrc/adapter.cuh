@@ -8,9 +8,9 @@
 // projections around the UNet's attention, with one style adapter per image of
 // the batch.
 //
-// A tile is 128 rows by bn columns.  While x's tile of 64 columns of C is in
-// shared memory for x W^T it also meets the D rows of the tile's adapters, so
-// z = x D^T costs 16 .. 64 more MMA columns and no second pass over x; z goes
+// A tile is 128 rows by bn columns.  The D rows of the tile's adapters lie
+// behind W's in shared memory, so one product of bn + 16 .. 64 columns gives
+// x W^T and z = x D^T side by side, with no second pass over x; z goes
 // from tensor memory through registers (scaled by s in fp32, zeroed in the
 // rows of other adapters, rounded to 16 bits: the next product's operand) back
 // to tensor memory, and as the A operand of z U^T adds onto the same fp32
@@ -42,27 +42,28 @@ enum : int { kAdapterNone = 0, kAdapterRows = 1, kAdapterMma = 2 };
 
 struct AdapterCfg {
   static constexpr int BK = 64;
-  static constexpr int BN = 192;                    // most columns per tile
+  static constexpr int BN = 160;                    // most columns per tile
   static constexpr int BN_ROWS = 64;                // with per-row adapters
   static constexpr int ZN = 64;                     // ranks per phase
   static constexpr int MAX_STAGES = 12;
   static constexpr int SLACK = 16384;               // kept behind the stages when x's tile is short: its products read up to 16 KB
   static constexpr int RING = 180224;               // bytes of the ring of stages, and with per-row adapters of z U^T behind it
   static constexpr int CORR = 128 * (BN_ROWS + 4) * 4;
-  static constexpr int OFF_PLAN = RING;
+  static constexpr int EPI = 16;                    // epilogue warps, four per quarter of a tile's rows
+  static constexpr int PW = 40;                     // most columns of an epilogue warp
+  static constexpr int OFF_STG = RING;              // [EPI] 32 rows of up to PW columns of y
+  static constexpr int STG = 32 * PW * 2;
   static constexpr int PLANS = 3;                   // tiles the planner may run ahead
   static constexpr int PLAN = 128 * 4 + 128 * 4 + 128 * 4 + 16;   // adapters, rows' places, rows' scales, count
-  static constexpr int EPI = 16;                    // epilogue warps, four per quarter of a tile's rows
-  static constexpr int OFF_STG = OFF_PLAN + PLANS * PLAN;   // [EPI] 32 rows of 32 columns, 80 bytes apart
-  static constexpr int STG = 32 * 80;
-  static constexpr int OFF_BIAS = OFF_STG + EPI * STG;      // [EPI] biases of up to 64 columns
-  static constexpr int OFF_BAR = OFF_BIAS + EPI * 64 * 4;
+  static constexpr int OFF_PLAN = OFF_STG + EPI * STG;
+  static constexpr int OFF_BIAS = OFF_PLAN + PLANS * PLAN;   // [EPI] biases of up to PW columns
+  static constexpr int OFF_BAR = OFF_BIAS + EPI * PW * 4;
   static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 2 * PLANS + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static constexpr int NTHREADS = (8 + EPI) * 32;   // TMA, MMA, planner, idle, epilogue, four that convert z
   static constexpr int CORR_THREADS = (4 + EPI) * 32;   // that compute z U^T of single rows
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr int TM_Z = 2 * BN;               // accumulators at 0 and BN, z at 384 and 448
+  static constexpr int TM_TILE = 256;               // tensor-memory columns of a tile: its accumulator, then z
   __host__ __device__ static constexpr int ring(int mode) { return mode == kAdapterRows ? RING - CORR : RING; }
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -75,7 +76,8 @@ struct AdapterParams {
   const void* U;          // ROWS: [L][K][R]
   void* Y;                // [T][K]
   int T, K, L, R, rows;   // rows: rows per id
-  int bn;                 // columns per tile: a multiple of 16 up to 192
+  int bn;                 // columns per tile: a multiple of 16 up to 160
+  int pw;                 // columns per epilogue warp: a multiple of 8 up to 40 that divides bn, bn / pw <= 4
   int tm;                 // rows per tile: 128, or all rows of a shorter x rounded up to 8
   int rts, nts;           // row tiles, column tiles
   int ksteps;             // ceil(C / 64)
@@ -130,8 +132,9 @@ struct AdapterPlan {
   int32_t adapter[128];   // the distinct adapters, in order of first appearance
   int32_t place[128];     // each row's place in that list, -1 without one
   float scale[128];       // each row's scale
-  int32_t count;
-  int32_t pad[3];
+  int32_t count;          // adapters
+  int32_t slots, phases;  // count * chunks, and the phases they fill (at least one)
+  int32_t pad;
 };
 static_assert(sizeof(AdapterPlan) == AdapterCfg::PLAN, "plan layout");
 
@@ -171,7 +174,7 @@ template <bool BF16, int MODE>
 __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     adapter_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
-                   const AdapterParams p) {
+                   const __grid_constant__ CUtensorMap tmY, const AdapterParams p) {
   using C = AdapterCfg;
   constexpr bool MMA = MODE == kAdapterMma, ROWS = MODE == kAdapterRows;
   extern __shared__ uint8_t smem_raw[];
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmY);
     if (MMA) {
       tma_prefetch_desc(&tmD);
       tma_prefetch_desc(&tmU);
@@ -237,9 +241,8 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // Phases of a tile of `count` adapters, and the slots of phase ph.
-  auto phases = [&](int count) { return max(1, (count * p.chunks + spp - 1) / spp); };
-  auto slots_of = [&](int count, int ph) { return min(spp, count * p.chunks - ph * spp); };
+  // slots of phase ph of a tile
+  auto slots_of = [&](int slots, int ph) { return min(spp, slots - ph * spp); };
 
   if (warp == 2) {
     // ------------------------------ planner -----------------------------------
@@ -278,7 +281,11 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           ++count;
         }
       }
-      if (lane == 0) pl->count = count;
+      if (lane == 0) {
+        pl->count = count;
+        pl->slots = count * p.chunks;
+        pl->phases = max(1, (count * p.chunks + spp - 1) / spp);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&plan_full[pb]);
     }
@@ -288,24 +295,30 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     uint32_t c = 0, ui = 0;
     bool live = true, pend = false, pend_last = false;
     int pend_ph = 0, pend_n0 = 0;
-    uint32_t pend_pb = 0;
+    uint32_t pend_pb = 0, pend_zr = 0;
     for (int u = blockIdx.x; live && (MMA || u < tiles); u += gridDim.x, ++ui) {
       const bool more = !MMA || u < tiles;      // one turn past the last tile: its last phase's U tiles
       if (MMA && u >= tiles && !pend) break;
       const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
       const uint32_t pb = ui % C::PLANS;
-      int count = 0;
+      int slots = 0, nph = 1;
       if (MMA && more) {
         live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
         if (!live) break;
-        count = plans[pb].count;
+        slots = plans[pb].slots;
+        nph = plans[pb].phases;
       }
-      const int nph = MMA && more ? phases(count) : 1, steps = more ? p.ksteps : 1;
+      const int steps = more ? p.ksteps : 1;
       for (int ph = 0; ph < nph && live; ++ph) {
-        const int ns = MMA && more ? slots_of(count, ph) : 0;
+        const int ns = MMA && more ? slots_of(slots, ph) : 0;
+        const uint32_t zr = (ui + ph) & 1;        // the tensor memory of this phase's z
+        // the last phase's U tiles: half way through this one's steps, or before
+        // them where this one's z takes the last one's place (after a tile of an
+        // even number of phases)
+        const int when = pend && pend_zr == zr ? -1 : mid;
         const uint32_t bytes = p.tm * 128 + (ph == 0 ? p.bn * 128 : 0) + ns * p.rc * 128;
-        for (int ks = 0; ks < steps; ks += p.sub) {
-          if (more) {
+        for (int ks = when < 0 ? -p.sub : 0; ks < steps; ks += p.sub) {
+          if (more && ks >= 0) {
             uint32_t st;
             live = ring.take(st, kSiteKEmpty, abort_flag);
             if (!live) break;
@@ -325,10 +338,10 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             }
             ++c;
           }
-          if (MMA && pend && (ks == mid || !more)) {
+          if (MMA && pend && (ks == mid || ks < 0 || !more)) {
             // the U tiles of the last phase, one stage per slot
             const AdapterPlan* pl = &plans[pend_pb];
-            const int nu = slots_of(pl->count, pend_ph);
+            const int nu = slots_of(pl->slots, pend_ph);
             for (int j = 0; j < nu; ++j) {
               uint32_t st;
               live = ring.take(st, kSiteKEmpty, abort_flag);
@@ -349,6 +362,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           pend_ph = ph;
           pend_n0 = n0;
           pend_pb = pb;
+          pend_zr = zr;
           pend_last = ph == nph - 1;
         } else if (MMA && more) {
           arrive_elect(smem_u32(&plan_empty[pb]));   // a tile without adapters
@@ -366,58 +380,58 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc_w = idesc_f16(128, p.bn, BF16, false, false);
     const uint64_t xdesc = sdesc_sw128(sbase, 16, 1024), wdesc = sdesc_sw128(sbase + off_w, 16, 1024);
-    const uint64_t ddesc = sdesc_sw128(sbase + off_d, 16, 1024);
+    const uint64_t ddesc = sdesc_sw128(sbase + off_d, 16, 1024);   // W's rows, then D's: one operand
     RingWalk ring(bfull, NS, 0);
     uint32_t ui = 0, zc = 0;                    // tiles, phases with adapters
     bool live = true, pend = false, pend_last = false;
-    int pend_ph = 0, pend_count = 0;
-    uint32_t pend_pb = 0, pend_ab = 0, pend_z = 0;
+    int pend_ph = 0, pend_slots = 0;
+    uint32_t pend_pb = 0, pend_ab = 0, pend_z = 0, pend_zr = 0;
     for (int u = blockIdx.x; live && (MMA || u < tiles); u += gridDim.x, ++ui) {
       const bool more = !MMA || u < tiles;      // as in the producer
       if (MMA && u >= tiles && !pend) break;
       const uint32_t ab = ui & 1, na = ui >> 1, pb = ui % C::PLANS;
-      int count = 0;
+      int slots = 0, nph = 1;
       if (more) {
         if (MMA) {
           live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
           if (!live) break;
-          count = plans[pb].count;
+          slots = plans[pb].slots;
+          nph = plans[pb].phases;
         }
         live = wait_warp(smem_u32(&acc_empty[ab]), (na & 1) ^ 1, kSiteAccEmpty, abort_flag);
         if (!live) break;
         tc_fence_after();
       }
-      const int nph = MMA && more ? phases(count) : 1, steps = more ? p.ksteps : 1;
+      const int steps = more ? p.ksteps : 1;
       for (int ph = 0; ph < nph && live; ++ph) {
-        const int ns = MMA && more ? slots_of(count, ph) : 0;
-        const uint32_t zb = zc & 1;
-        const uint32_t idesc_d = idesc_f16(128, max(ns, 1) * p.rc, BF16, false, false);
-        for (int ks = 0; ks < steps; ks += p.sub) {
-          if (more) {
+        const int ns = MMA && more ? slots_of(slots, ph) : 0;
+        const uint32_t zb = zc & 1, zr = (ui + ph) & 1;
+        const int when = pend && pend_zr == zr ? -1 : mid;   // as in the producer
+        // phase 0: W's columns and the adapters' in one product; later ones: the adapters' alone
+        const uint32_t idesc = idesc_f16(128, ph == 0 ? p.bn + ns * p.rc : max(ns, 1) * p.rc, BF16, false, false);
+        const uint32_t dst = tmem + zr * C::TM_TILE + (ph == 0 ? 0 : p.bn);
+        const uint64_t opdesc = ph == 0 ? wdesc : ddesc;
+        for (int ks = when < 0 ? -p.sub : 0; ks < steps; ks += p.sub) {
+          if (more && ks >= 0) {
             uint32_t st;
             live = ring.take(st, kSiteKFull, abort_flag);
             if (!live) break;
             tc_fence_after();
-            const uint64_t off = st * (p.stage >> 4);
-            const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
-            const bool two = p.sub == 2 && ks + 1 < steps;
-            if (ph == 0) {
-              mma_ss4(tmem + ab * C::BN, xdesc + off, wdesc + off, idesc_w, ks > 0, 2, 2);
-              if (two) mma_ss4(tmem + ab * C::BN, xdesc + off2, wdesc + off2, idesc_w, 1, 2, 2);
-            }
-            if (MMA && ns > 0) {
-              mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off, ddesc + off, idesc_d, ks > 0, 2, 2);
-              if (two) mma_ss4(tmem + C::TM_Z + zb * C::ZN, xdesc + off2, ddesc + off2, idesc_d, 1, 2, 2);
+            const uint64_t off = st * (static_cast<uint32_t>(p.stage) >> 4);
+            mma_ss4(dst, xdesc + off, opdesc + off, idesc, ks > 0, 2, 2);
+            if (p.sub == 2 && ks + 1 < steps) {
+              const uint64_t off2 = off + (static_cast<uint32_t>(sub) >> 4);
+              mma_ss4(dst, xdesc + off2, opdesc + off2, idesc, 1, 2, 2);
             }
             mma_commit_at(bempty + 8 * st);
           }
-          if (MMA && pend && (ks == mid || !more)) {
+          if (MMA && pend && (ks == mid || ks < 0 || !more)) {
             // z U^T of the last phase onto its tile's accumulator
             const uint32_t pz = pend_z & 1;
             live = wait_warp(smem_u32(&p_full[pz]), (pend_z >> 1) & 1, kSitePFull, abort_flag);
             if (!live) break;
             tc_fence_after();
-            const int nu = slots_of(pend_count, pend_ph);
+            const int nu = slots_of(pend_slots, pend_ph);
             for (int j = 0; j < nu; ++j) {
               uint32_t st;
               live = ring.take(st, kSiteVFull, abort_flag);
@@ -426,7 +440,8 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
               const uint64_t ud = wdesc + st * (p.stage >> 4);
               for (int kk = 0; kk < p.rc / 16; ++kk) {
                 const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column
-                mma_ts(tmem + pend_ab * C::BN, tmem + C::TM_Z + pz * C::ZN + r / 32 * 32 + r % 32 / 2, ud + 2 * kk, idesc_w, 1u);
+                mma_ts(tmem + pend_ab * C::TM_TILE, tmem + pend_zr * C::TM_TILE + p.bn + r / 32 * 32 + r % 32 / 2,
+                       ud + 2 * kk, idesc_w, 1u);
               }
               mma_commit_at(bempty + 8 * st);
               }
@@ -443,10 +458,11 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           mma_commit_at(smem_u32(&z_full[zb]));
           pend = true;
           pend_ph = ph;
-          pend_count = count;
+          pend_slots = slots;
           pend_pb = pb;
           pend_ab = ab;
           pend_z = zc++;
+          pend_zr = zr;
           pend_last = ph == nph - 1;
         } else {
           mma_commit_at(smem_u32(&acc_full[ab]));
@@ -478,20 +494,20 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
       if (!live) break;
       const AdapterPlan* pl = &plans[pb];
-      const int count = pl->count, place = pl->place[r];
+      const int count = pl->count, slots = pl->slots, tile_phases = pl->phases, place = pl->place[r];
       const float scale = pl->scale[r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&plan_empty[pb]);
-      const int nph = count > 0 ? phases(count) : 0;
+      const int nph = count > 0 ? tile_phases : 0;
       for (int ph = 0; ph < nph; ++ph, ++zc) {
         const uint32_t zb = zc & 1;
         live = wait_warp(smem_u32(&z_full[zb]), (zc >> 1) & 1, kSiteSFull, abort_flag);
         if (!live) break;
         tc_fence_after();
-        const int ranks = slots_of(count, ph) * p.rc;
+        const int ranks = slots_of(slots, ph) * p.rc;
 #pragma unroll 1
         for (int j0 = 0; j0 < ranks; j0 += 32) {
-          const uint32_t zt = tmem + C::TM_Z + zb * C::ZN + j0 + lane_off;
+          const uint32_t zt = tmem + ((ui + ph) & 1) * C::TM_TILE + p.bn + j0 + lane_off;
           uint32_t v[32], w[16];
           tmem_ld_x32(zt, v);
           tmem_wait_ld();
@@ -520,18 +536,18 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stg = smem + C::OFF_STG + (warp - 4) * C::STG;
-    float* sb = reinterpret_cast<float*>(smem + C::OFF_BIAS) + (warp - 4) * 64;
+    float* sb = reinterpret_cast<float*>(smem + C::OFF_BIAS) + (warp - 4) * C::PW;
+    const int c0 = part * p.pw;                 // this warp's columns of a tile
     uint32_t ui = 0;
     for (int u = blockIdx.x; u < tiles; u += gridDim.x, ++ui) {
       const uint32_t ab = ui & 1, na = ui >> 1;
       const int rt = u / p.nts, n0 = (u - rt * p.nts) * p.bn;
-      const int r = quarter * 32 + lane, row = rt * p.tm + r;
+      const int r = quarter * 32 + lane;
       const int rows = min(min(p.tm - quarter * 32, 32), p.T - rt * p.tm - quarter * 32);   // of this warp
+      const bool mine = c0 < p.bn && n0 + c0 < p.K && rows > 0;
       __syncwarp();
-      for (int c0 = part * 32, i = lane; c0 < p.bn; c0 += 128, i += 32) {
-        const int n = n0 + c0 + lane;
-        sb[i] = p.bias != nullptr && n < p.K ? __ldg(p.bias + n) : 0.f;
-      }
+      for (int i = lane; mine && i < p.pw; i += 32)
+        sb[i] = p.bias != nullptr && n0 + c0 + i < p.K ? __ldg(p.bias + n0 + c0 + i) : 0.f;
       if constexpr (ROWS) {
         adapter_corr<BF16>(p, corr, rt * p.tm, n0);
         named_bar_sync(1, C::CORR_THREADS);
@@ -541,56 +557,62 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       // a CTA that gives up keeps its barriers' company to the last tile
       if (!live && !ROWS) break;
       tc_fence_after();
-      // 32 columns at a time (the last ones 16), the four warps of a quarter in turn
-      const float* bs = sb;
-#pragma unroll 1
-      for (int c0 = part * 32; live && c0 < p.bn && n0 + c0 < p.K && rows > 0; c0 += 128, bs += 32) {
-        uint32_t v[32];
-        tmem_ld_x32(tmem + ab * C::BN + c0 + lane_off, v);
+      // The sums come into registers first, so that the next tile but one can
+      // have their place while they are stored: its products wait for that.
+      constexpr int PW = ROWS ? C::BN_ROWS / 4 : C::PW;
+      uint32_t v[PW];
+      if (mine) {
+#pragma unroll
+        for (int j = 0; j < PW; j += 8)
+          if (j < p.pw) tmem_ld_x8(tmem + ab * C::TM_TILE + c0 + j + lane_off, v + j);
         tmem_wait_ld();
-        reg_fence<32>(v);
-        const int cols = min(min(p.bn - c0, 32), p.K - n0 - c0);   // a multiple of 8
-        float f[32];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 b = reinterpret_cast<const float4*>(bs)[q];
-          f[4 * q] = __uint_as_float(v[4 * q]) + b.x;
-          f[4 * q + 1] = __uint_as_float(v[4 * q + 1]) + b.y;
-          f[4 * q + 2] = __uint_as_float(v[4 * q + 2]) + b.z;
-          f[4 * q + 3] = __uint_as_float(v[4 * q + 3]) + b.w;
-        }
-        if constexpr (ROWS) {
-          const float4* cr = reinterpret_cast<const float4*>(corr + r * (p.bn + 4) + c0);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (4 * q < cols) {
-              const float4 b = cr[q];
-              f[4 * q] += b.x;
-              f[4 * q + 1] += b.y;
-              f[4 * q + 2] += b.z;
-              f[4 * q + 3] += b.w;
-            }
-          }
-        }
-        // through shared memory, so that a warp stores 8 rows of 64 bytes at once
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + lane * 80 + 16 * q) = pack8<BF16>(f + 8 * q);
-        __syncwarp();
-        uint8_t* dst = static_cast<uint8_t*>(p.Y) + (static_cast<int64_t>(rt * p.tm + quarter * 32) * p.K + n0 + c0) * 2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2), ch = lane & 3;
-          if (rr < rows && ch * 8 < cols)
-            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(rr) * p.K * 2 + ch * 16) =
-                *reinterpret_cast<const uint4*>(stg + rr * 80 + ch * 16);
-        }
+        reg_fence<PW>(v);
       }
-      if constexpr (ROWS) named_bar_sync(2, C::CORR_THREADS);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      if (mine && live) {
+        if (lane == 0) bulk_wait_read<0>();     // the piece before has been read
+        __syncwarp();
+        // rows of 2 pw bytes as TMA takes them
+#pragma unroll
+        for (int j = 0; j < PW; j += 8) {
+          if (j < p.pw) {
+            float f[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 b = reinterpret_cast<const float4*>(sb + j)[q];
+              f[4 * q] = __uint_as_float(v[j + 4 * q]) + b.x;
+              f[4 * q + 1] = __uint_as_float(v[j + 4 * q + 1]) + b.y;
+              f[4 * q + 2] = __uint_as_float(v[j + 4 * q + 2]) + b.z;
+              f[4 * q + 3] = __uint_as_float(v[j + 4 * q + 3]) + b.w;
+            }
+            if constexpr (ROWS) {
+              if (lane < rows) {
+                const float4* cr = reinterpret_cast<const float4*>(corr + r * (p.bn + 4) + c0 + j);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const float4 b = cr[q];
+                  f[4 * q] += b.x;
+                  f[4 * q + 1] += b.y;
+                  f[4 * q + 2] += b.z;
+                  f[4 * q + 3] += b.w;
+                }
+              }
+            }
+            *reinterpret_cast<uint4*>(stg + lane * 2 * p.pw + 2 * j) = pack8<BF16>(f);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmY, stg, n0 + c0, rt * p.tm + quarter * 32, 0);   // clipped at T and K
+          bulk_commit();
+        }
+      }
+      if constexpr (ROWS) named_bar_sync(2, C::CORR_THREADS);
     }
+    if (lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();

@@ -389,7 +389,8 @@ size_t adapter_ws_bytes(const sdattn_adapter_desc* d) {
   return adapter_rows(d) ? static_cast<size_t>(d->T) * d->R * sizeof(float) : 0;
 }
 
-// Columns per tile (a multiple of 16 up to `most`): the fewest waves of the
+// Columns per tile (16, 48, or a multiple of 32, up to `most`, so that equal
+// pieces of whole 16-byte units go to at most four warps): the fewest waves of the
 // longest of a tile's products (2 clocks per column and 64 of C, the adapters'
 // ranks included), issue (300 clocks a step), loads (45 bytes per clock and SM)
 // and epilogue, plus one epilogue at the end.
@@ -399,6 +400,7 @@ int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int most, int nsm
   int best_bn = most;
   double best = 1e300;
   for (int bn = most; bn >= 16; bn -= 16) {
+    if (bn % 32 != 0 && bn != 16 && bn != 48) continue;
     const int64_t tiles = rts * ((d->K + bn - 1) / bn);
     const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
     const double step = std::max(std::max(2.0 * (bn + rc), 300.0), 128.0 * (tm + bn + rc) / 45.0);
@@ -446,9 +448,12 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.stage = p.sub * step;
   p.stages = std::min(Cfg::MAX_STAGES, room / p.stage);
   const CUtensorMapDataType dt = elem16(d->dtype);
-  CUtensorMap mx, mw, md, mu;
+  CUtensorMap mx, mw, md, mu, my;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, K, 1, C * 2, K * C * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
+  p.pw = (p.bn + 31) / 32 * 8;
+  if (!make_map_3d(&my, Y, dt, K, T, 1, K * 2, T * K * 2, static_cast<uint32_t>(p.pw), 32, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return SDATTN_ERR_CUDA;
   if (MMA) {
     if (!make_map_3d(&md, D, dt, C, R, L, C * 2, R * C * 2, 64, static_cast<uint32_t>(p.rc))) return SDATTN_ERR_CUDA;
     if (!make_map_3d(&mu, U, dt, R, K, L, R * 2, K * R * 2, 64, static_cast<uint32_t>(p.bn))) return SDATTN_ERR_CUDA;
@@ -466,7 +471,7 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, Cfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(nsm, int64_t(p.rts) * p.nts));
-  return launch(kern, grid, Cfg::NTHREADS, Cfg::SMEM, s, mx, mw, md, mu, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+  return launch(kern, grid, Cfg::NTHREADS, Cfg::SMEM, s, mx, mw, md, mu, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 template <bool BF16>

@@ -239,10 +239,17 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   CUtensorMap mx, mw, my;
   if (!make_map_3d(&mx, X, dt, C, T, 1, C * 2, T * C * 2, 64, static_cast<uint32_t>(p.tm))) return SDATTN_ERR_CUDA;
   if (!make_map_3d(&mw, W, dt, C, F, 2, C * 2, F * C * 2, 64, static_cast<uint32_t>(p.hn))) return SDATTN_ERR_CUDA;
-  const uint64_t ldy = BWD ? 4 * F : 2 * F;   // bytes of a row of y, or of P = [dh, dg]
-  if (!make_map_3d(&my, Y, dt, F, T, BWD ? 2 : 1, ldy, BWD ? 2 * F : T * ldy, BWD ? 32 : 64, 32,
-                   BWD ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
-    return SDATTN_ERR_CUDA;
+  // y, or the two halves of P = [dh, dg], and dy as the pairs' warps move them
+  const uint64_t ldy = BWD ? 4 * F : 2 * F;
+  CUtensorMap mdy, mdg;
+  if (!make_map_3d(&my, Y, dt, F, T, 1, ldy, T * ldy, 64, 32)) return SDATTN_ERR_CUDA;
+  if (BWD) {
+    if (!make_map_3d(&mdy, dY, dt, F, T, 1, F * 2, T * F * 2, 64, 32)) return SDATTN_ERR_CUDA;
+    if (!make_map_3d(&mdg, static_cast<uint16_t*>(Y) + F, dt, F, T, 1, ldy, T * ldy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return SDATTN_ERR_CUDA;
+  } else {
+    mdy = mdg = my;   // never read
+  }
   const int64_t tiles = int64_t(p.rts) * p.fts;
   if (plan.pair) {
     auto kern = sdattn::gated_kernel<BF16, BWD, true>;
@@ -250,14 +257,14 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
     static std::atomic<uint64_t> done{0};
     if (!ensure_smem(kern, smem, done, dev)) return SDATTN_ERR_CUDA;
     const int grid = static_cast<int>(std::min<int64_t>(nsm / 2, tiles)) * 2;
-    return launch_cluster(kern, grid, 2, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+    return launch_cluster(kern, grid, 2, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, mdy, mdg, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
   }
   auto kern = sdattn::gated_kernel<BF16, BWD, false>;
   constexpr int smem = sdattn::GatedSmem<BWD, false>::BYTES;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, smem, done, dev)) return SDATTN_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(nsm, tiles));
-  return launch(kern, grid, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
+  return launch(kern, grid, sdattn::GatedCfg::NTHREADS, smem, s, mx, mw, my, mdy, mdg, p) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 // dx = P W and dW = P^T x: tiles, splits and where their partials lie.

@@ -242,10 +242,11 @@ sdattn_status launch_gated(const sdattn_ff_desc* d, const void* X, const void* W
   // y, or the two halves of P = [dh, dg], and dy as the pairs' warps move them
   const uint64_t ldy = BWD ? 4 * F : 2 * F;
   CUtensorMap mdy, mdg;
-  if (!make_map_3d(&my, Y, dt, F, T, 1, ldy, T * ldy, 64, 32)) return SDATTN_ERR_CUDA;
+  constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_map_3d(&my, Y, dt, F, T, 1, ldy, T * ldy, 32, 32, sw)) return SDATTN_ERR_CUDA;
   if (BWD) {
-    if (!make_map_3d(&mdy, dY, dt, F, T, 1, F * 2, T * F * 2, 64, 32)) return SDATTN_ERR_CUDA;
-    if (!make_map_3d(&mdg, static_cast<uint16_t*>(Y) + F, dt, F, T, 1, ldy, T * ldy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_map_3d(&mdy, dY, dt, F, T, 1, F * 2, T * F * 2, 32, 32, sw)) return SDATTN_ERR_CUDA;
+    if (!make_map_3d(&mdg, static_cast<uint16_t*>(Y) + F, dt, F, T, 1, ldy, T * ldy, 32, 32, sw))
       return SDATTN_ERR_CUDA;
   } else {
     mdy = mdg = my;   // never read

@@ -101,8 +101,8 @@ struct GatedCfg {
   static constexpr int BK = 64;                     // columns of C per stage
   static constexpr int A_BYTES = 128 * 128;         // 128 rows of x
   static constexpr int HN = 128;                    // most columns of h (and of g) per tile
-  static constexpr int EPI = 8;                     // epilogue warps of a tile
-  static constexpr int NTHREADS = (4 + 2 * EPI) * 32;   // TMA, MMA, bias, one idle warp, two groups of epilogue warps
+  static constexpr int EPI = 16;                    // epilogue warps
+  static constexpr int NTHREADS = (4 + EPI) * 32;   // TMA, MMA, bias, one idle warp, epilogue
   static constexpr uint32_t TMEM_COLS = 512;        // two accumulators of 2 HN columns
 };
 
@@ -112,17 +112,17 @@ struct GatedCfg {
 template <bool BWD, bool PAIR>
 struct GatedSmem {
   static constexpr int STAGE = 2 * 128 * 128;       // PAIR
-  static constexpr int STAGES = BWD ? 3 : 4;        // PAIR
+  static constexpr int STAGES = BWD ? 4 : 5;        // PAIR
   static constexpr int RING = PAIR ? STAGES * STAGE : 212992;
   static constexpr int SLACK = 16384;               // kept behind the stages when x's tile is short: its products read up to 16 KB
   static constexpr int MAX_STAGES = 12;
-  // an epilogue warp's staging (PAIR): 32 rows x 64 columns of y; backward: of
-  // dy, which dh replaces in place, and 32 rows x 32 columns of dg
-  static constexpr int WSTG = PAIR ? (BWD ? 6144 : 4096) : 0;
+  // an epilogue warp's staging (PAIR): 32 rows x 32 columns of y; backward: of
+  // dy, which dh replaces in place, and of dg
+  static constexpr int WSTG = PAIR ? (BWD ? 4096 : 2048) : 0;
   static constexpr int OFF_STG = RING;
-  static constexpr int OFF_BIAS = OFF_STG + 2 * GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
+  static constexpr int OFF_BIAS = OFF_STG + GatedCfg::EPI * WSTG;   // [2 tiles][h, g][HN] fp32
   static constexpr int OFF_BAR = OFF_BIAS + 2 * 2 * GatedCfg::HN * 4;
-  static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 1 + (PAIR && BWD ? 2 * GatedCfg::EPI : 0);
+  static constexpr int NBAR = 2 * MAX_STAGES + 4 + 4 + 1 + (PAIR && BWD ? GatedCfg::EPI : 0);
   static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory budget");
 };
@@ -173,13 +173,13 @@ __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t
 // Roles: warp 0 TMA (a ring of x / W stages), warp 1 MMA (tcgen05 SS,
 // 128 or, in a pair, 256 x 2 hn x 16; two accumulators so that a tile's
 // epilogue overlaps the next tile's products), warp 2 the tiles' biases, warps
-// 4..19 epilogue: two groups of eight on alternate tiles, so that one group's
-// waits and hand-offs pass under the other's arithmetic; in a group two warps
-// per quarter of the CTA's 128 rows, dividing the tile's columns.  (16 images
-// at 64x64: one group of eight warps 123 us, one of sixteen 117 us.)
+// 4..19 epilogue: four warps per quarter of the CTA's 128 rows, dividing the
+// tile's columns.  (The epilogue sets the pace: eight warps took 123 us for 16
+// images at 64x64, two groups of eight on alternate tiles lose where a CTA has
+// an odd handful of tiles.)
 // PAIR: tiles of 256 rows by 128 columns of h, a CTA of the pair holding the h
 // rows of W's tile and the other the g rows; the results leave through shared
-// memory and TMA stores of 32 rows x 64 columns of y or dh, or 32 of dg, which
+// memory and TMA stores of 32 rows x 32 columns of y, or of dh and of dg, which
 // also clip at the edges.  Backward: a warp's dy arrives by TMA while it waits
 // for the products (read from global memory where it was used, its latency set
 // the pace: 37 us for the 64x64 pair).
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   uint64_t* bias_full = acc_empty + 2;       // [2] bias warp -> epilogue
   uint64_t* bias_empty = bias_full + 2;      // [2] back
   uint64_t* drain_bar = bias_empty + 2;
-  uint64_t* dy_full = drain_bar + 1;         // backward pairs: [2 EPI] each epilogue warp's dy
+  uint64_t* dy_full = drain_bar + 1;         // backward pairs: [EPI] each epilogue warp's dy
   float* sbias = reinterpret_cast<float*>(smem + S::OFF_BIAS);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + S::NBAR);   // [0] tensor memory, [1] abort
   volatile uint32_t* abort_flag = misc + 1;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
     }
     mbar_init(drain_bar, 1);
     if (PAIR && BWD)
-      for (int i = 0; i < 2 * C::EPI; ++i) mbar_init(&dy_full[i], 1);
+      for (int i = 0; i < C::EPI; ++i) mbar_init(&dy_full[i], 1);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -376,35 +376,39 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
   } else if (warp >= 4) {
     // ------------------------------ epilogue ----------------------------------
     constexpr int CW = PAIR ? 16 : 8;             // columns per pass
-    const int quarter = warp & 3, part = (warp - 4) >> 2 & 1, grp = (warp - 4) >> 3;
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stg = smem + S::OFF_STG + (warp - 4) * S::WSTG;
     const uint32_t dyb = smem_u32(&dy_full[warp - 4]), dys = smem_u32(stg);
     uint32_t loads = 0;
-    // this warp's dy of tile u: 64 columns of its 32 rows
+    // this warp's dy of tile u: 32 columns of its 32 rows
     auto load_dy = [&](int u) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
-      expect_tx_elect(dyb, 4096);
-      load_elect(dys, &tmDY, ft * hn + part * 64, rt * TROWS + rank * 128 + quarter * 32, 0, dyb);
+      expect_tx_elect(dyb, 2048);
+      load_elect(dys, &tmDY, ft * hn + part * 32, rt * TROWS + rank * 128 + quarter * 32, 0, dyb);
       ++loads;
     };
-    uint32_t na = 0;                              // tiles of this group
-    if (PAIR && BWD && u0 + grp * ustep < tiles) load_dy(u0 + grp * ustep);
-    for (int u = u0 + grp * ustep; u < tiles; u += 2 * ustep, ++na) {
+    uint32_t ui = 0;
+    if (PAIR && BWD && u0 < tiles) load_dy(u0);
+    for (int u = u0; u < tiles; u += ustep, ++ui) {
       const int rt = u / p.fts, ft = u - rt * p.fts;
-      const uint32_t ab = grp;
+      const uint32_t ab = ui & 1, na = ui >> 1;
       const int r0 = rt * TROWS + rank * 128 + quarter * 32, row = r0 + lane;
       const bool row_ok = row < p.T;
       const uint16_t* dy_row = static_cast<const uint16_t*>(p.dY) + static_cast<int64_t>(row) * p.F + ft * hn;
-      // PAIR: this warp's 64 columns; otherwise every other 8 columns
-      const int first = PAIR ? part * 64 : part * 8, step = PAIR ? CW : 16, last = PAIR ? first + 64 : hn;
+      // PAIR: this warp's 32 columns; otherwise every fourth 8 columns
+      const int first = PAIR ? part * 32 : part * 8, step = PAIR ? CW : 32, last = PAIR ? first + 32 : hn;
       uint4 next_dy = make_uint4(0, 0, 0, 0);     // without pairs: loaded one pass ahead
       if (BWD && !PAIR && row_ok && ft * hn + first < p.F) next_dy = __ldg(reinterpret_cast<const uint4*>(dy_row + first));
       if (!wait_warp(smem_u32(&bias_full[ab]), na & 1, kSiteVFull, abort_flag) ||
           !wait_warp(bacc_full + 8 * ab, na & 1, kSiteAccFull, abort_flag))
         break;
       tc_fence_after();
-      if (PAIR && BWD && !wait_warp(dyb, na & 1, kSiteQFull, abort_flag)) break;
+      if (PAIR && BWD && !wait_warp(dyb, ui & 1, kSiteQFull, abort_flag)) break;
+      if (PAIR && !BWD) {
+        if (lane == 0) bulk_wait_read<0>();       // the buffer's previous store has read it
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int c0 = first; c0 < last; c0 += step) {
         const int f = ft * hn + c0;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         if constexpr (BWD && PAIR) {
 #pragma unroll
           for (int q = 0; q < CW / 8; ++q)        // zeros past T and F
-            dy[q] = *reinterpret_cast<const uint4*>(stg + lane * 128 + ((((c0 & 63) / 8 + q) ^ (lane & 7)) << 4));
+            dy[q] = *reinterpret_cast<const uint4*>(stg + lane * 64 + ((((c0 & 31) / 8 + q) ^ (lane >> 1 & 3)) << 4));
         } else if constexpr (BWD) {
           dy[0] = next_dy;
           next_dy = row_ok && c0 + step < last && f + step < p.F ? __ldg(reinterpret_cast<const uint4*>(dy_row + c0 + step))
@@ -454,29 +458,21 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         for (int q = 0; q < CW / 8; ++q)
           gated_columns8<BWD, BF16>(h + 8 * q, g + 8 * q, bh + 8 * q, bh + 128 + 8 * q, dy[q], o0 + 8 * q, o1 + 8 * q);
         if constexpr (PAIR) {
-          if (BWD ? (c0 & 63) == 32 : c0 == first) {
-            if (lane == 0) bulk_wait_read<0>();   // the buffer's previous store has read it
-            __syncwarp();
-          }
 #pragma unroll
           for (int q = 0; q < CW / 8; ++q) {
-            // rows of 128 bytes, 128-byte swizzle: chunk ^ row
-            const int ch = (((c0 & 63) / 8 + q) ^ (lane & 7)) << 4;
-            *reinterpret_cast<uint4*>(stg + lane * 128 + ch) = pack8<BF16>(o0 + 8 * q);
-            if constexpr (BWD) {
-              // rows of 64 bytes, 64-byte swizzle: chunk ^ row / 2
-              const int cg = (((c0 & 31) / 8 + q) ^ (lane >> 1 & 3)) << 4;
-              *reinterpret_cast<uint4*>(stg + 4096 + lane * 64 + cg) = pack8<BF16>(o1 + 8 * q);
-            }
+            // rows of 64 bytes, 64-byte swizzle: chunk ^ row / 2
+            const int ch = (((c0 & 31) / 8 + q) ^ (lane >> 1 & 3)) << 4;
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ch) = pack8<BF16>(o0 + 8 * q);
+            if constexpr (BWD) *reinterpret_cast<uint4*>(stg + 2048 + lane * 64 + ch) = pack8<BF16>(o1 + 8 * q);
           }
-          if (BWD ? (c0 & 31) == 16 : c0 + CW == last) {
+          if (c0 + CW == last) {
             fence_proxy_async_smem();
             __syncwarp();
             // stores start inside the tensor; what runs over its edges is clipped
             const int fs = ft * hn + first;
-            if (lane == 0 && r0 < p.T) {
-              if (c0 + CW == last && fs < p.F) tma_store_3d(&tmY, stg, fs, r0, 0);
-              if (BWD && fs + (c0 & 32) < p.F) tma_store_3d(&tmDG, stg + 4096, fs + (c0 & 32), r0, 0);
+            if (lane == 0 && r0 < p.T && fs < p.F) {
+              tma_store_3d(&tmY, stg, fs, r0, 0);
+              if constexpr (BWD) tma_store_3d(&tmDG, stg + 2048, fs, r0, 0);
               bulk_commit();
             }
           }
@@ -487,11 +483,12 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         }
         if constexpr (BWD) {
           if (p.part != nullptr) {
-            // rows past T add nothing, whatever their biases are
+            if (r0 + 32 > p.T) {                  // rows past T add nothing, whatever their biases are
 #pragma unroll
-            for (int j = 0; j < CW; ++j) {
-              o0[j] = row_ok ? o0[j] : 0.f;
-              o1[j] = row_ok ? o1[j] : 0.f;
+              for (int j = 0; j < CW; ++j) {
+                o0[j] = row_ok ? o0[j] : 0.f;
+                o1[j] = row_ok ? o1[j] : 0.f;
+              }
             }
             const float s0 = warp_column_sums<CW>(o0, lane), s1 = warp_column_sums<CW>(o1, lane);
             const int j = lane / (32 / CW);
@@ -513,10 +510,10 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
           mbar_arrive(&acc_empty[ab]);
         }
       }
-      if (PAIR && BWD && u + 2 * ustep < tiles) { // the next tile's dy, over dh once its store has read it
+      if (PAIR && BWD && u + ustep < tiles) {     // the next tile's dy, over dh once its store has read it
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        load_dy(u + 2 * ustep);
+        load_dy(u + ustep);
       }
     }
     if (PAIR && BWD && loads > 0) {               // the last dy has landed, also where the loop gave up

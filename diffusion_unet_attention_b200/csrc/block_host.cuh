@@ -358,16 +358,27 @@ sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const 
   const int grid = std::min(nsm / 2, pl.pp.s[0].units + pl.pp.s[1].units) * 2;
   if (!launch_cluster(kern, grid, 2, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
     return SDATTN_ERR_CUDA;
+  sdattn::FinishParams f = {};
+  int64_t work = 0;
   for (int i = 0; i < 2; ++i) {
     const sdattn::ProductSide& sd = pl.pp.s[i];
     if (sd.splits == 1) continue;
-    const int64_t n = static_cast<int64_t>(sd.M) * sd.N;
-    const int g = static_cast<int>(std::min<int64_t>((n / 8 + 255) / 256, int64_t(nsm) * 8));
-    if (!launch(sdattn::add_splits_kernel<BF16>, g, 256, 0, s, parts[i], sd.splits, n, outs[i])) return SDATTN_ERR_CUDA;
+    f.part[i] = parts[i];
+    f.out[i] = outs[i];
+    f.n[i] = static_cast<int64_t>(sd.M) * sd.N;
+    f.splits[i] = sd.splits;
+    work = std::max(work, f.n[i] / 8);
   }
-  if (dbias && !launch_column_sum(db_part, (d->T + 31) / 32, 2 * d->F, 2 * d->F, dbias, dbias, s))
-    return SDATTN_ERR_CUDA;
-  return SDATTN_OK;
+  f.first = static_cast<int>(std::min<int64_t>((work + 127) / 128, int64_t(nsm) * 2));
+  if (dbias) {
+    f.db_part = db_part;
+    f.db = dbias;
+    f.rows = (d->T + 31) / 32;
+    f.cols = 2 * d->F;
+  }
+  const int blocks = f.first + (dbias ? (f.cols + 31) / 32 : 0);
+  if (blocks == 0) return SDATTN_OK;
+  return launch(sdattn::finish_kernel<BF16>, blocks, 1024, 0, s, f) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 // --------------------------------------------------------------------------

@@ -12,7 +12,7 @@
 //
 // gated_kernel     x, W (, dy) -> y, or P in 16 bits and partial sums of db
 // product_kernel   P, W, x -> dx and dW, one launch for both products
-// add_splits_kernel  partial products of a split contraction -> dx, dW
+// finish_kernel    partial products of a split contraction -> dx, dW; partial sums -> db
 //
 // All products run on the tensor cores (fp32 accumulators in tensor memory);
 // bias, activation and gradients are fp32.  Roundings to 16 bits: y, dx, dW
@@ -28,6 +28,7 @@
 // g_f in the same tensor-memory lane, HN columns apart.
 #pragma once
 
+#include "layer_norm.cuh"
 #include "pipeline.cuh"
 #include "unet_ops.cuh"
 
@@ -409,6 +410,20 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         if (lane == 0) bulk_wait_read<0>();       // the buffer's previous store has read it
         __syncwarp();
       }
+      // The accumulator is free once the warp's last columns are in registers:
+      // the next tile but one's products wait for it, not for the arithmetic.
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) {
+            arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
+          } else {
+            mbar_arrive(&acc_empty[ab]);
+          }
+        }
+      };
+      if (first >= last) release();               // a narrow tile without columns for this warp
 #pragma unroll 1
       for (int c0 = first; c0 < last; c0 += step) {
         const int f = ft * hn + c0;
@@ -452,6 +467,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
             g[j] = __float_as_uint(__uint_as_float(g[j]) + __uint_as_float(g2[j]));
           }
         }
+        if (c0 + step >= last) release();
         const float* bh = sbias + ab * 256 + c0;
         float o0[CW], o1[CW];
 #pragma unroll
@@ -500,16 +516,8 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
           }
         }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bias_empty[ab]);
-        if constexpr (PAIR) {
-          arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
-        } else {
-          mbar_arrive(&acc_empty[ab]);
-        }
-      }
+      if (lane == 0) mbar_arrive(&bias_empty[ab]);
       if (PAIR && BWD && u + ustep < tiles) {     // the next tile's dy, over dh once its store has read it
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 // Each CTA of a pair holds its 128 rows of A and half of the tile's columns of
 // B.  M- and N-major tiles are slabs of 64 columns x 64 contraction rows,
 // 128-byte swizzled.  A result whose contraction is split goes to fp32
-// partials that add_splits_kernel adds in split order.
+// partials that finish_kernel adds in split order.
 // ---------------------------------------------------------------------------
 struct ProductCfg {
   static constexpr int BK = 64;
@@ -782,23 +790,47 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
   }
 }
 
-// out[i] = sum over splits of part[split][i], in split order, n a multiple of 8.
+// What remains after the products, in one launch: the split results' sums, out[i]
+// = sum over splits of part[split][i] in split order (n a multiple of 8), and db
+// from its partial rows (blocks from `first` on, as in column_sum_kernel).
+struct FinishParams {
+  const float* part[2];   // null where a side was not split
+  void* out[2];
+  int64_t n[2];
+  int splits[2];
+  const float* db_part;   // [rows][cols], or null
+  float* db;
+  int64_t rows;
+  int cols;
+  int first;              // blocks of the split results
+};
+
 template <bool BF16>
-__global__ void __launch_bounds__(256) add_splits_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                         void* __restrict__ out) {
+__global__ void __launch_bounds__(1024) finish_kernel(const FinishParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n / 8; i += stride) {
-    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (static_cast<int>(blockIdx.x) >= p.first) {
+    column_sum_block(p.db_part, p.rows, p.cols, p.cols, p.db, p.db, blockIdx.x - p.first);
+    return;
+  }
+  const int64_t stride = static_cast<int64_t>(p.first) * blockDim.x;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    if (p.part[side] == nullptr) continue;
+    const int64_t n = p.n[side];
+    // a warp's 32 pieces together, warps dealt over the blocks
+    const int64_t i0 = (static_cast<int64_t>(threadIdx.x >> 5) * p.first + blockIdx.x) * 32 + (threadIdx.x & 31);
+    for (int64_t i = i0; i < n / 8; i += stride) {
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(part + s * n) + 2 * i;
-      const float4 u = __ldcs(src), v = __ldcs(src + 1);
-      a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
-      a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+      for (int s = 0; s < p.splits[side]; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(p.part[side] + s * n) + 2 * i;
+        const float4 u = __ldcs(src), v = __ldcs(src + 1);
+        a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+        a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+      }
+      reinterpret_cast<uint4*>(p.out[side])[i] = pack8<BF16>(a);
     }
-    reinterpret_cast<uint4*>(out)[i] = pack8<BF16>(a);
   }
 }
 

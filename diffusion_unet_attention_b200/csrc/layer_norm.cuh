@@ -321,19 +321,18 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
 }
 
 // Adds P partial rows of n floats, column by column and in a fixed order: 32
-// columns per CTA, 32 threads per column over rows r, r + 32, ..., then the 32
-// sums in order.  The first n0 columns go to out0, the others to out1.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int64_t P, int n, int n0,
-                                                          float* __restrict__ out0, float* __restrict__ out1) {
+// columns per block of 1024 threads, 32 threads per column over rows r, r + 32,
+// ..., then the 32 sums in order.  The first n0 columns go to out0, the others
+// to out1.
+__device__ __forceinline__ void column_sum_block(const float* part, int64_t P, int n, int n0, float* out0, float* out1,
+                                                 int block) {
   __shared__ float s[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + cx;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  const int j = block * 32 + cx;
   float a = 0.f;
   if (j < n) {
-#pragma unroll 4
-    for (int64_t r = ry; r < P; r += 32) a += part[r * n + j];
+#pragma unroll 8
+    for (int64_t r = ry; r < P; r += 32) a += __ldcg(part + r * n + j);
   }
   s[ry][cx] = a;
   __syncthreads();
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   float t = s[cx][ry];
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  const int jj = blockIdx.x * 32 + ry;
+  const int jj = block * 32 + ry;
   if (cx == 0 && jj < n) {
     if (jj < n0) {
       out0[jj] = t;
@@ -349,6 +348,13 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
       out1[jj - n0] = t;
     }
   }
+}
+
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int64_t P, int n, int n0, float* out0,
+                                                          float* out1) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  column_sum_block(part, P, n, n0, out0, out1, blockIdx.x);
 }
 
 }  // namespace sdattn

@@ -383,7 +383,7 @@ size_t sdattn_gated_ff_bwd_workspace_bytes(const sdattn_ff_desc* desc);
  * dX [T][C], dW [2F][C]: outputs of type dtype, rounded once; dbias: output
  * or NULL.  With T = 0 dW and dbias are zero-filled.  Every sum has a fixed
  * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-
- * owned, overwritten, no state between calls.  Up to five launches. */
+ * owned, overwritten, no state between calls.  Up to three launches. */
 sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, const void* X, const void* W,
                                   const float* bias, void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes,
                                   void* stream);

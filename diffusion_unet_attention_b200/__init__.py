@@ -430,7 +430,7 @@ def _call(device: torch.device, fn, *args) -> None:
     """Calls the library's function `fn` with `device` current, the stream (the
     last argument) being the device's current one; raises on a status."""
     at = device.index
-    if at == torch.cuda.current_device():
+    if at == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(at))
     else:
         with torch.cuda.device(device):
@@ -439,17 +439,11 @@ def _call(device: torch.device, fn, *args) -> None:
         _lib.check(fn.__name__, st)
 
 
-def _same_device(x: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must live on {x.device}")
-
-
 def _vector(t: torch.Tensor | None, n: int, device: torch.device, name: str) -> torch.Tensor | None:
     """A parameter vector as contiguous fp32 [n] on `device`, on a 16-byte boundary."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
     if t.dtype is not torch.float32 or t.device != device:
         t = t.to(device=device, dtype=torch.float32)
@@ -462,6 +456,11 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+def _meta(t: torch.Tensor | None):
+    """What the argument checks of a call read of a tensor."""
+    return None if t is None else (t.shape, t.dtype, t.device)
+
+
 def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
     """The output: `out` if it fits, else a new tensor of x's dtype."""
     if out is None:
@@ -471,33 +470,35 @@ def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
     return out
 
 
-# Descriptors and workspace sizes follow from the shapes alone, so the last
-# few are kept: building one again costs more of the host's time than the rest
-# of its call.
-@functools.lru_cache(maxsize=256)
-def _shape(kind, *fields):
-    return ctypes.byref(kind(*fields))
-
-
-@functools.lru_cache(maxsize=256)
-def _bytes(device: torch.device, fn: str, kind, *fields) -> int:
+def _bytes(device: torch.device, fn: str, desc) -> int:
     with torch.cuda.device(device):
-        return int(getattr(_lib_handle(), fn)(_shape(kind, *fields)))
+        return int(getattr(_lib_handle(), fn)(desc))
 
 
+# The checks below read shapes, dtypes and devices alone, and so do descriptors
+# and workspace sizes; the last few are kept, since making them again costs more
+# of the host's time than the rest of a call.
 _LN_DTYPES = {**_DTYPES, torch.float32: _lib.SDATTN_F32}
 
 
-def _ln_fields(x: torch.Tensor, eps: float):
-    if not x.is_cuda or x.dim() < 1:
+@functools.lru_cache(maxsize=256)
+def _ln_plan(xm, eps: float, dym=None, statsm=None, backward: bool = False):
+    shape, dtype, device = xm
+    if device.type != "cuda" or len(shape) < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
-    dt = _LN_DTYPES.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"dtype {x.dtype} not supported (float16, bfloat16 or float32)")
-    C = x.shape[-1]
+    if dtype not in _LN_DTYPES:
+        raise TypeError(f"dtype {dtype} not supported (float16, bfloat16 or float32)")
+    C = shape[-1]
     if C < 1:
         raise ValueError("rows must have at least one value")
-    return x.numel() // C, C, dt, float(eps)
+    desc = ctypes.byref(_lib.LNDesc(math.prod(shape) // C, C, _LN_DTYPES[dtype], eps))
+    if not backward:
+        return desc, C, 0
+    if dym != xm:
+        raise ValueError("dy must match x in shape, dtype and device")
+    if statsm != (shape[:-1] + (2,), torch.float32, device):
+        raise ValueError("stats must be layer_norm's fp32 [..., 2] on x's device")
+    return desc, C, _bytes(device, "sdattn_layer_norm_bwd_workspace_bytes", desc)
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -507,14 +508,13 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
 
     With `return_stats` returns (y, stats), stats [..., 2] fp32 = (mean,
     1 / sqrt(var + eps)) of every row, as `layer_norm_backward` takes it."""
-    fields = _ln_fields(x, eps)
-    dev, C = x.device, fields[1]
+    dev = x.device
+    desc, C, _ = _ln_plan((x.shape, x.dtype, dev), float(eps))
     g, b = _vector(gamma, C, dev, "gamma"), _vector(beta, C, dev, "beta")
     x = _contig(x)
     y = torch.empty_like(x) if out is None else _out(out, x, x.shape)
     stats = x.new_empty(x.shape[:-1] + (2,), dtype=torch.float32) if return_stats else None
-    _call(dev, _lib_handle().sdattn_layer_norm, _shape(_lib.LNDesc, *fields), x.data_ptr(), _ptr(g), _ptr(b),
-          y.data_ptr(), _ptr(stats))
+    _call(dev, _lib_handle().sdattn_layer_norm, desc, x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
     return (y, stats) if return_stats else y
 
 
@@ -522,36 +522,36 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     """Gradients of `layer_norm`: (dx, dgamma, dbeta) from dy (x's shape and
     dtype), the forward's x and stats, and gamma.  dx has x's dtype, dgamma and
     dbeta are fp32 [C]; repeated calls give identical bits."""
-    fields = _ln_fields(x, 0.0)
-    dev, C = x.device, fields[1]
-    _same_device(x, dy=dy, stats=stats)
-    if dy.shape != x.shape or dy.dtype != x.dtype:
-        raise ValueError("dy must match x in shape and dtype")
-    if stats.shape != x.shape[:-1] + (2,) or stats.dtype != torch.float32:
-        raise ValueError("stats must be layer_norm's fp32 [..., 2]")
+    dev = x.device
+    desc, C, need = _ln_plan((x.shape, x.dtype, dev), 0.0, _meta(dy), _meta(stats), True)
     g = _vector(gamma, C, dev, "gamma")
     dy, x, stats = _contig(dy), _contig(x), _contig(stats)
     dx, dg, db = torch.empty_like(x), x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
-    need = _bytes(dev, "sdattn_layer_norm_bwd_workspace_bytes", _lib.LNDesc, *fields)
     ws = x.new_empty(need, dtype=torch.uint8)
-    _call(dev, _lib_handle().sdattn_layer_norm_bwd, _shape(_lib.LNDesc, *fields), dy.data_ptr(), x.data_ptr(),
-          stats.data_ptr(), _ptr(g), dx.data_ptr(), dg.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
+    _call(dev, _lib_handle().sdattn_layer_norm_bwd, desc, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
+          dx.data_ptr(), dg.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
     return dx, dg, db
 
 
-def _ff_fields(x: torch.Tensor, w: torch.Tensor):
-    if not x.is_cuda or x.dim() < 1:
+@functools.lru_cache(maxsize=256)
+def _ff_plan(xm, wm, dym=None, backward: bool = False):
+    shape, dtype, device = xm
+    if device.type != "cuda" or len(shape) < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
-    dt = _DTYPES.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"dtype {x.dtype} not supported (float16 or bfloat16)")
-    C = x.shape[-1]
-    if w.dim() != 2 or w.shape[1] != C or w.shape[0] % 2 or w.dtype != x.dtype:
-        raise ValueError(f"w must be [2F, {C}] of x's dtype")
-    _same_device(x, w=w)
-    if C < 1 or w.shape[0] < 2:
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype {dtype} not supported (float16 or bfloat16)")
+    C = shape[-1]
+    if len(wm[0]) != 2 or wm[0][1] != C or wm[0][0] % 2 or wm[1:] != (dtype, device):
+        raise ValueError(f"w must be [2F, {C}] of x's dtype, on its device")
+    F = wm[0][0] // 2
+    if C < 1 or F < 1:
         raise ValueError("widths must be at least 1")
-    return x.numel() // C, C, w.shape[0] // 2, dt
+    desc, yshape = ctypes.byref(_lib.FFDesc(math.prod(shape) // C, C, F, _DTYPES[dtype])), shape[:-1] + (F,)
+    if not backward:
+        return desc, F, yshape, 0
+    if dym != (yshape, dtype, device):
+        raise ValueError(f"dy must be x.shape[:-1] + ({F},) of x's dtype, on its device")
+    return desc, F, yshape, _bytes(device, "sdattn_gated_ff_bwd_workspace_bytes", desc)
 
 
 def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None):
@@ -560,12 +560,12 @@ def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
 
     x [..., C] and w [2F, C] (fp16 or bf16), fp32 bias [2F] or None; returns
     [..., F].  C and F must be multiples of 8."""
-    fields = _ff_fields(x, w)
-    b = _vector(bias, 2 * fields[2], x.device, "bias")
+    dev = x.device
+    desc, F, yshape, _ = _ff_plan((x.shape, x.dtype, dev), _meta(w))
+    b = _vector(bias, 2 * F, dev, "bias")
     x, w = _contig(x), _contig(w)
-    y = _out(out, x, x.shape[:-1] + (fields[2],))
-    _call(x.device, _lib_handle().sdattn_gated_ff, _shape(_lib.FFDesc, *fields), x.data_ptr(), w.data_ptr(), _ptr(b),
-          y.data_ptr())
+    y = _out(out, x, yshape)
+    _call(dev, _lib_handle().sdattn_gated_ff, desc, x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
     return y
 
 
@@ -574,20 +574,55 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     forward's inputs (the projection is computed again).  dx and dw have x's
     dtype; dbias is fp32 [2F], or None without a bias.  Repeated calls give
     identical bits."""
-    fields = _ff_fields(x, w)
-    dev, F = x.device, fields[2]
-    _same_device(x, dy=dy)
-    if dy.shape != x.shape[:-1] + (F,) or dy.dtype != x.dtype:
-        raise ValueError(f"dy must be x.shape[:-1] + ({F},) of x's dtype")
+    dev = x.device
+    desc, F, _, need = _ff_plan((x.shape, x.dtype, dev), _meta(w), _meta(dy), True)
     b = _vector(bias, 2 * F, dev, "bias")
     dy, x, w = _contig(dy), _contig(x), _contig(w)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     db = x.new_empty(2 * F, dtype=torch.float32) if bias is not None else None
-    need = _bytes(dev, "sdattn_gated_ff_bwd_workspace_bytes", _lib.FFDesc, *fields)
     ws = x.new_empty(need, dtype=torch.uint8)
-    _call(dev, _lib_handle().sdattn_gated_ff_bwd, _shape(_lib.FFDesc, *fields), dy.data_ptr(), x.data_ptr(),
-          w.data_ptr(), _ptr(b), dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), need)
+    _call(dev, _lib_handle().sdattn_gated_ff_bwd, desc, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
+          dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), need)
     return dx, dw, db
+
+
+@functools.lru_cache(maxsize=256)
+def _adapter_plan(xm, wm, downm, upm, scalem, idsm):
+    shape, dtype, device = xm
+    if device.type != "cuda" or len(shape) < 1:
+        raise ValueError("x must be a CUDA tensor [G, ..., C]")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype {dtype} not supported (float16 or bfloat16)")
+    C = shape[-1]
+    if len(wm[0]) != 2 or wm[0][1] != C or wm[1] != dtype:
+        raise ValueError(f"w must be [K, {C}] of x's dtype")
+    K = wm[0][0]
+    if C < 1 or K < 1:
+        raise ValueError("widths must be at least 1")
+    for name, m in (("w", wm), ("down", downm), ("up", upm), ("scale", scalem), ("ids", idsm)):
+        if m is not None and m[2] != device:
+            raise ValueError(f"{name} must live on {device}")
+    T, L, R, rows = math.prod(shape) // C, 0, 0, 1
+    if idsm is None:
+        if downm is not None or upm is not None or scalem is not None:
+            raise ValueError("adapters need ids")
+    else:
+        if len(shape) < 2 or idsm[0] != shape[:1] or idsm[1] != torch.int32:
+            raise ValueError("ids must be int32 [G] for x [G, ..., C]")
+        if downm is None or upm is None or len(downm[0]) != 3 or downm[0][2] != C:
+            raise ValueError(f"down must be [L, R, {C}]")
+        L, R = downm[0][:2]
+        if upm[0] != (L, K, R) or downm[1] != dtype or upm[1] != dtype:
+            raise ValueError(f"up must be [{L}, {K}, {R}], down and up of x's dtype")
+        if scalem is not None and scalem[0] != (L,):
+            raise ValueError(f"scale must be [{L}]")
+        if L == 0 or R == 0:                # nothing to add
+            L = R = 0
+        else:
+            rows = max(T // max(shape[0], 1), 1)
+    desc = ctypes.byref(_lib.AdapterDesc(T, C, K, L, R, rows, _DTYPES[dtype]))
+    need = _bytes(device, "sdattn_adapter_linear_workspace_bytes", desc) if L else 0
+    return desc, K, L, shape[:-1] + (K,), need
 
 
 def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
@@ -606,44 +641,21 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
     be multiples of 8 (pad smaller ranks with zeros once), R at most 256.
     For requests of different lengths pass their rows as x [T, C] with one id a
     row.  Returns [G, ..., K]."""
-    if not x.is_cuda or x.dim() < 1:
-        raise ValueError("x must be a CUDA tensor [G, ..., C]")
-    if x.dtype not in _DTYPES:
-        raise TypeError(f"dtype {x.dtype} not supported (float16 or bfloat16)")
-    C = x.shape[-1]
-    if w.dim() != 2 or w.shape[1] != C or w.dtype != x.dtype:
-        raise ValueError(f"w must be [K, {C}] of x's dtype")
-    K = w.shape[0]
-    if C < 1 or K < 1:
-        raise ValueError("widths must be at least 1")
-    _same_device(x, w=w, down=down, up=up, scale=scale, ids=ids)
-    T, L, R, rows = x.numel() // C, 0, 0, 1
-    if ids is None:
-        if down is not None or up is not None or scale is not None:
-            raise ValueError("adapters need ids")
-    else:
-        if x.dim() < 2 or ids.shape != x.shape[:1] or ids.dtype != torch.int32:
-            raise ValueError("ids must be int32 [G] for x [G, ..., C]")
-        if down is None or up is None or down.dim() != 3 or down.shape[2] != C:
-            raise ValueError(f"down must be [L, R, {C}]")
-        L, R = down.shape[:2]
-        if up.shape != (L, K, R) or down.dtype != x.dtype or up.dtype != x.dtype:
-            raise ValueError(f"up must be [{L}, {K}, {R}], down and up of x's dtype")
-        if L == 0 or R == 0:                # nothing to add
-            ids = down = up = scale = None
-            L = R = 0
-        else:
-            rows = max(T // max(x.shape[0], 1), 1)
-            scale = _vector(scale, L, x.device, "scale")
-            ids, down, up = _contig(ids), _contig(down), _contig(up)
-    b = _vector(bias, K, x.device, "bias")
+    dev = x.device
+    desc, K, L, yshape, need = _adapter_plan((x.shape, x.dtype, dev), _meta(w), _meta(down), _meta(up), _meta(scale),
+                                             _meta(ids))
+    b = _vector(bias, K, dev, "bias")
     x, w = _contig(x), _contig(w)
-    y = _out(out, x, x.shape[:-1] + (K,))
-    fields = (T, C, K, L, R, rows, _DTYPES[x.dtype])
-    need = _bytes(x.device, "sdattn_adapter_linear_workspace_bytes", _lib.AdapterDesc, *fields) if L else 0
+    y = _out(out, x, yshape)
+    if not L:
+        _call(dev, _lib_handle().sdattn_adapter_linear, desc, x.data_ptr(), w.data_ptr(), _ptr(b), None, None, None, None,
+              y.data_ptr(), None, 0)
+        return y
+    scale = _vector(scale, L, dev, "scale")
+    ids, down, up = _contig(ids), _contig(down), _contig(up)
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    _call(x.device, _lib_handle().sdattn_adapter_linear, _shape(_lib.AdapterDesc, *fields), x.data_ptr(), w.data_ptr(),
-          _ptr(b), _ptr(down), _ptr(up), _ptr(scale), _ptr(ids), y.data_ptr(), _ptr(ws), need)
+    _call(dev, _lib_handle().sdattn_adapter_linear, desc, x.data_ptr(), w.data_ptr(), _ptr(b), down.data_ptr(),
+          up.data_ptr(), _ptr(scale), ids.data_ptr(), y.data_ptr(), _ptr(ws), need)
     return y
 
 

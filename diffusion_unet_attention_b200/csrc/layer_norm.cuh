@@ -18,7 +18,8 @@
 // The weight's gradients: every CTA runs over rows b, b + grid, ... and keeps
 // the sums of its columns in registers (a lane owns the same columns of every
 // row it sees), adds its warps' sums in warp order and writes one partial
-// row of 2C floats; a second kernel adds the partial rows in a fixed order.
+// row of 2C floats; a second kernel adds the partial rows in a fixed order
+// (with one CTA its sums are the result).
 // No atomics: repeated calls give identical bits.
 #pragma once
 
@@ -107,7 +108,9 @@ struct LNParams {
   const float* gamma;   // may be null (ones)
   const float* beta;    // may be null (zeros)
   float* stats;         // [T][2]: mean, 1 / sqrt(var + eps)  (forward: may be null)
-  float* part;          // backward: [grid][2C] partial column sums
+  float* part0;         // backward: partial sums of dgamma and dbeta, CTA b's at + b * pitch
+  float* part1;
+  int64_t pitch;
   int64_t T;
   int C;
   int nch;              // accesses of E elements per row
@@ -266,7 +269,8 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
       }
     }
   }
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
+  float* out0 = p.part0 + blockIdx.x * p.pitch;
+  float* out1 = p.part1 + blockIdx.x * p.pitch;
   if constexpr (CTA) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -274,8 +278,8 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
       if (i < p.nch)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          out[i * E + e] = ag[u][e];
-          out[p.C + i * E + e] = ab[u][e];
+          out0[i * E + e] = ag[u][e];
+          out1[i * E + e] = ab[u][e];
         }
     }
   } else {
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_b
       for (int j = threadIdx.x; j < p.C; j += blockDim.x) {
         float t = colsum[j];
         for (int w = 1; w < nw; ++w) t += colsum[w * p.C + j];
-        out[side * p.C + j] = t;
+        (side ? out1 : out0)[j] = t;
       }
       __syncthreads();
     }

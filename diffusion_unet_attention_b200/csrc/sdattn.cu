@@ -1148,12 +1148,15 @@ sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, 
   p.dX = dX;
   p.gamma = gamma;
   p.stats = const_cast<float*>(stats);
-  p.part = static_cast<float*>(ws);
+  float* part = static_cast<float*>(ws);
+  p.part0 = grid == 1 ? dgamma : part;
+  p.part1 = grid == 1 ? dbeta : part + desc->C;
+  p.pitch = 2 * int64_t(desc->C);
   if (grid > 0) {
     const sdattn_status r = launch_ln(desc, p, pl, true, grid, s);
-    if (r != SDATTN_OK) return r;
+    if (r != SDATTN_OK || grid == 1) return r;
   }
-  return launch_column_sum(p.part, grid, 2 * desc->C, desc->C, dgamma, dbeta, s) ? SDATTN_OK : SDATTN_ERR_CUDA;
+  return launch_column_sum(part, grid, 2 * desc->C, desc->C, dgamma, dbeta, s) ? SDATTN_OK : SDATTN_ERR_CUDA;
 }
 
 sdattn_status sdattn_gated_ff(const sdattn_ff_desc* desc, const void* X, const void* W, const float* bias, void* Y,

@@ -345,7 +345,7 @@ size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc);
  * dY, X, stats, gamma (or NULL: ones): inputs; dX, dgamma, dbeta (float32
  * [C]): outputs, all written (zero sums when T = 0).  The sums run in a fixed
  * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-
- * owned, overwritten, no state between calls.  Two launches. */
+ * owned, overwritten, no state between calls.  At most two launches. */
 sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, const void* X, const float* stats,
                                     const float* gamma, void* dX, float* dgamma, float* dbeta, void* ws,
                                     size_t ws_bytes, void* stream);

@@ -426,27 +426,27 @@ def wino_workspace_bytes(N: int, C: int, K: int, H: int, W: int, dtype=torch.flo
     return int(_lib_handle().sdattn_wino_workspace_bytes(ctypes.byref(_conv_desc(N, C, K, H, W, dtype))))
 
 
-def _call(device: torch.device, fn, *args) -> None:
-    """Calls the library's function `fn` with `device` current, the stream (the
-    last argument) being the device's current one; raises on a status."""
-    at = device.index
+def _call(at: int, name: str, *args) -> None:
+    """Calls the library's function `name` with CUDA device `at` current, the
+    stream (the last argument) being that device's current one; raises on a status."""
+    fn = getattr(_lib._lib or _lib.load(), name)
     if at == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(at))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(at):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(at))
     if st != 0:
-        _lib.check(fn.__name__, st)
+        _lib.check(name, st)
 
 
-def _vector(t: torch.Tensor | None, n: int, device: torch.device, name: str) -> torch.Tensor | None:
-    """A parameter vector as contiguous fp32 [n] on `device`, on a 16-byte boundary."""
+def _vector(t: torch.Tensor | None, n: int, at: int, name: str) -> torch.Tensor | None:
+    """A parameter vector as contiguous fp32 [n] on CUDA device `at`, on a 16-byte boundary."""
     if t is None:
         return None
     if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
-    if t.dtype is not torch.float32 or t.device != device:
-        t = t.to(device=device, dtype=torch.float32)
+    if t.dtype is not torch.float32 or t.get_device() != at:
+        t = t.to(device=torch.device("cuda", at), dtype=torch.float32)
     if not t.is_contiguous() or t.data_ptr() % 16:
         t = t.clone(memory_format=torch.contiguous_format)      # a slice of a larger tensor
     return t
@@ -457,8 +457,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _meta(t: torch.Tensor | None):
-    """What the argument checks of a call read of a tensor."""
-    return None if t is None else (t.shape, t.dtype, t.device)
+    """What the argument checks of a call read of a tensor (device -1: not CUDA)."""
+    return None if t is None else (t.shape, t.dtype, t.get_device())
 
 
 def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
@@ -470,8 +470,8 @@ def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
     return out
 
 
-def _bytes(device: torch.device, fn: str, desc) -> int:
-    with torch.cuda.device(device):
+def _bytes(at: int, fn: str, desc) -> int:
+    with torch.cuda.device(at):
         return int(getattr(_lib_handle(), fn)(desc))
 
 
@@ -483,8 +483,8 @@ _LN_DTYPES = {**_DTYPES, torch.float32: _lib.SDATTN_F32}
 
 @functools.lru_cache(maxsize=256)
 def _ln_plan(xm, eps: float, dym=None, statsm=None, backward: bool = False):
-    shape, dtype, device = xm
-    if device.type != "cuda" or len(shape) < 1:
+    shape, dtype, at = xm
+    if at < 0 or len(shape) < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
     if dtype not in _LN_DTYPES:
         raise TypeError(f"dtype {dtype} not supported (float16, bfloat16 or float32)")
@@ -496,9 +496,9 @@ def _ln_plan(xm, eps: float, dym=None, statsm=None, backward: bool = False):
         return desc, C, 0
     if dym != xm:
         raise ValueError("dy must match x in shape, dtype and device")
-    if statsm != (shape[:-1] + (2,), torch.float32, device):
+    if statsm != (shape[:-1] + (2,), torch.float32, at):
         raise ValueError("stats must be layer_norm's fp32 [..., 2] on x's device")
-    return desc, C, _bytes(device, "sdattn_layer_norm_bwd_workspace_bytes", desc)
+    return desc, C, _bytes(at, "sdattn_layer_norm_bwd_workspace_bytes", desc)
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -508,13 +508,13 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
 
     With `return_stats` returns (y, stats), stats [..., 2] fp32 = (mean,
     1 / sqrt(var + eps)) of every row, as `layer_norm_backward` takes it."""
-    dev = x.device
-    desc, C, _ = _ln_plan((x.shape, x.dtype, dev), float(eps))
-    g, b = _vector(gamma, C, dev, "gamma"), _vector(beta, C, dev, "beta")
+    at = x.get_device()
+    desc, C, _ = _ln_plan((x.shape, x.dtype, at), float(eps))
+    g, b = _vector(gamma, C, at, "gamma"), _vector(beta, C, at, "beta")
     x = _contig(x)
     y = torch.empty_like(x) if out is None else _out(out, x, x.shape)
     stats = x.new_empty(x.shape[:-1] + (2,), dtype=torch.float32) if return_stats else None
-    _call(dev, _lib_handle().sdattn_layer_norm, desc, x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
+    _call(at, "sdattn_layer_norm", desc, x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
     return (y, stats) if return_stats else y
 
 
@@ -522,26 +522,26 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     """Gradients of `layer_norm`: (dx, dgamma, dbeta) from dy (x's shape and
     dtype), the forward's x and stats, and gamma.  dx has x's dtype, dgamma and
     dbeta are fp32 [C]; repeated calls give identical bits."""
-    dev = x.device
-    desc, C, need = _ln_plan((x.shape, x.dtype, dev), 0.0, _meta(dy), _meta(stats), True)
-    g = _vector(gamma, C, dev, "gamma")
+    at = x.get_device()
+    desc, C, need = _ln_plan((x.shape, x.dtype, at), 0.0, _meta(dy), _meta(stats), True)
+    g = _vector(gamma, C, at, "gamma")
     dy, x, stats = _contig(dy), _contig(x), _contig(stats)
     dx, dg, db = torch.empty_like(x), x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
     ws = x.new_empty(need, dtype=torch.uint8)
-    _call(dev, _lib_handle().sdattn_layer_norm_bwd, desc, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
+    _call(at, "sdattn_layer_norm_bwd", desc, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
           dx.data_ptr(), dg.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
     return dx, dg, db
 
 
 @functools.lru_cache(maxsize=256)
 def _ff_plan(xm, wm, dym=None, backward: bool = False):
-    shape, dtype, device = xm
-    if device.type != "cuda" or len(shape) < 1:
+    shape, dtype, at = xm
+    if at < 0 or len(shape) < 1:
         raise ValueError("x must be a CUDA tensor [..., C]")
     if dtype not in _DTYPES:
         raise TypeError(f"dtype {dtype} not supported (float16 or bfloat16)")
     C = shape[-1]
-    if len(wm[0]) != 2 or wm[0][1] != C or wm[0][0] % 2 or wm[1:] != (dtype, device):
+    if len(wm[0]) != 2 or wm[0][1] != C or wm[0][0] % 2 or wm[1:] != (dtype, at):
         raise ValueError(f"w must be [2F, {C}] of x's dtype, on its device")
     F = wm[0][0] // 2
     if C < 1 or F < 1:
@@ -549,9 +549,9 @@ def _ff_plan(xm, wm, dym=None, backward: bool = False):
     desc, yshape = ctypes.byref(_lib.FFDesc(math.prod(shape) // C, C, F, _DTYPES[dtype])), shape[:-1] + (F,)
     if not backward:
         return desc, F, yshape, 0
-    if dym != (yshape, dtype, device):
+    if dym != (yshape, dtype, at):
         raise ValueError(f"dy must be x.shape[:-1] + ({F},) of x's dtype, on its device")
-    return desc, F, yshape, _bytes(device, "sdattn_gated_ff_bwd_workspace_bytes", desc)
+    return desc, F, yshape, _bytes(at, "sdattn_gated_ff_bwd_workspace_bytes", desc)
 
 
 def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None):
@@ -560,12 +560,12 @@ def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
 
     x [..., C] and w [2F, C] (fp16 or bf16), fp32 bias [2F] or None; returns
     [..., F].  C and F must be multiples of 8."""
-    dev = x.device
-    desc, F, yshape, _ = _ff_plan((x.shape, x.dtype, dev), _meta(w))
-    b = _vector(bias, 2 * F, dev, "bias")
+    at = x.get_device()
+    desc, F, yshape, _ = _ff_plan((x.shape, x.dtype, at), _meta(w))
+    b = _vector(bias, 2 * F, at, "bias")
     x, w = _contig(x), _contig(w)
     y = _out(out, x, yshape)
-    _call(dev, _lib_handle().sdattn_gated_ff, desc, x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
+    _call(at, "sdattn_gated_ff", desc, x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
     return y
 
 
@@ -574,22 +574,22 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     forward's inputs (the projection is computed again).  dx and dw have x's
     dtype; dbias is fp32 [2F], or None without a bias.  Repeated calls give
     identical bits."""
-    dev = x.device
-    desc, F, _, need = _ff_plan((x.shape, x.dtype, dev), _meta(w), _meta(dy), True)
-    b = _vector(bias, 2 * F, dev, "bias")
+    at = x.get_device()
+    desc, F, _, need = _ff_plan((x.shape, x.dtype, at), _meta(w), _meta(dy), True)
+    b = _vector(bias, 2 * F, at, "bias")
     dy, x, w = _contig(dy), _contig(x), _contig(w)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     db = x.new_empty(2 * F, dtype=torch.float32) if bias is not None else None
     ws = x.new_empty(need, dtype=torch.uint8)
-    _call(dev, _lib_handle().sdattn_gated_ff_bwd, desc, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
+    _call(at, "sdattn_gated_ff_bwd", desc, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
           dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), need)
     return dx, dw, db
 
 
 @functools.lru_cache(maxsize=256)
 def _adapter_plan(xm, wm, downm, upm, scalem, idsm):
-    shape, dtype, device = xm
-    if device.type != "cuda" or len(shape) < 1:
+    shape, dtype, at = xm
+    if at < 0 or len(shape) < 1:
         raise ValueError("x must be a CUDA tensor [G, ..., C]")
     if dtype not in _DTYPES:
         raise TypeError(f"dtype {dtype} not supported (float16 or bfloat16)")
@@ -600,8 +600,8 @@ def _adapter_plan(xm, wm, downm, upm, scalem, idsm):
     if C < 1 or K < 1:
         raise ValueError("widths must be at least 1")
     for name, m in (("w", wm), ("down", downm), ("up", upm), ("scale", scalem), ("ids", idsm)):
-        if m is not None and m[2] != device:
-            raise ValueError(f"{name} must live on {device}")
+        if m is not None and m[2] != at:
+            raise ValueError(f"{name} must live on cuda:{at}")
     T, L, R, rows = math.prod(shape) // C, 0, 0, 1
     if idsm is None:
         if downm is not None or upm is not None or scalem is not None:
@@ -621,7 +621,7 @@ def _adapter_plan(xm, wm, downm, upm, scalem, idsm):
         else:
             rows = max(T // max(shape[0], 1), 1)
     desc = ctypes.byref(_lib.AdapterDesc(T, C, K, L, R, rows, _DTYPES[dtype]))
-    need = _bytes(device, "sdattn_adapter_linear_workspace_bytes", desc) if L else 0
+    need = _bytes(at, "sdattn_adapter_linear_workspace_bytes", desc) if L else 0
     return desc, K, L, shape[:-1] + (K,), need
 
 
@@ -641,20 +641,20 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
     be multiples of 8 (pad smaller ranks with zeros once), R at most 256.
     For requests of different lengths pass their rows as x [T, C] with one id a
     row.  Returns [G, ..., K]."""
-    dev = x.device
-    desc, K, L, yshape, need = _adapter_plan((x.shape, x.dtype, dev), _meta(w), _meta(down), _meta(up), _meta(scale),
+    at = x.get_device()
+    desc, K, L, yshape, need = _adapter_plan((x.shape, x.dtype, at), _meta(w), _meta(down), _meta(up), _meta(scale),
                                              _meta(ids))
-    b = _vector(bias, K, dev, "bias")
+    b = _vector(bias, K, at, "bias")
     x, w = _contig(x), _contig(w)
     y = _out(out, x, yshape)
     if not L:
-        _call(dev, _lib_handle().sdattn_adapter_linear, desc, x.data_ptr(), w.data_ptr(), _ptr(b), None, None, None, None,
+        _call(at, "sdattn_adapter_linear", desc, x.data_ptr(), w.data_ptr(), _ptr(b), None, None, None, None,
               y.data_ptr(), None, 0)
         return y
-    scale = _vector(scale, L, dev, "scale")
+    scale = _vector(scale, L, at, "scale")
     ids, down, up = _contig(ids), _contig(down), _contig(up)
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    _call(dev, _lib_handle().sdattn_adapter_linear, desc, x.data_ptr(), w.data_ptr(), _ptr(b), down.data_ptr(),
+    _call(at, "sdattn_adapter_linear", desc, x.data_ptr(), w.data_ptr(), _ptr(b), down.data_ptr(),
           up.data_ptr(), _ptr(scale), ids.data_ptr(), y.data_ptr(), _ptr(ws), need)
     return y
 

@@ -273,29 +273,32 @@ struct FFBwdPlan {
   sdattn::ProductParams pp;
   size_t p_bytes, db_bytes, part_bytes[2];
   size_t total;
+  int pairs;          // CTA pairs of the products' launch
 };
 
-// A result's columns are cut into the fewest tiles of at most 256, rounded up
-// to whole slabs of 64.  With L the contraction steps a pair of SMs would run if both
-// products were shared out evenly, a contraction longer than 3/4 L is split
-// into pieces of about L / 2 (at least 8 steps: a piece costs a partial
+// Up to 320 columns of a result are one tile; more are cut into the fewest
+// tiles of at most 256, rounded up to whole slabs of 64 (at 640 columns two
+// wide tiles took 4 us more than three with two accumulators).  With L the contraction steps a pair of SMs would run
+// if both products were shared out evenly, a contraction longer than 5/4 L is
+// split into pieces of at most L (at least 8 steps: a piece costs a partial
 // result that is written and read again).
 FFBwdPlan plan_ff_bwd(const sdattn_ff_desc* d, int nsm) {
   FFBwdPlan pl;
+  const int pairs = std::max(1, nsm / 2);
   const int M[2] = {static_cast<int>(d->T), 2 * d->F}, K[2] = {2 * d->F, static_cast<int>(d->T)};
   double total = 0;
   for (int i = 0; i < 2; ++i) {
     sdattn::ProductSide& s = pl.pp.s[i];
     s.M = M[i];
     s.N = d->C;
-    const int n = (s.N + 255) / 256;
+    const int most = s.N <= sdattn::ProductCfg::BN ? sdattn::ProductCfg::BN : 256, n = (s.N + most - 1) / most;
     s.bn = ((s.N + n - 1) / n + 63) / 64 * 64;
     s.nts = (s.N + s.bn - 1) / s.bn;
     s.mn = (s.M + 255) / 256 * s.nts;
     s.ksteps = (K[i] + 63) / 64;
     total += static_cast<double>(s.mn) * s.ksteps;
   }
-  const double L = total / (nsm / 2);
+  const double L = total / pairs;
   size_t at = 0;
   auto place = [&](size_t bytes) { at += (bytes + 255) / 256 * 256; return bytes; };
   pl.p_bytes = place(static_cast<size_t>(d->T) * 2 * d->F * 2);
@@ -303,14 +306,19 @@ FFBwdPlan plan_ff_bwd(const sdattn_ff_desc* d, int nsm) {
   for (int i = 0; i < 2; ++i) {
     sdattn::ProductSide& s = pl.pp.s[i];
     s.splits = 1;
-    if (s.ksteps > 0.75 * L)
-      s.splits = std::max(1, std::min(s.ksteps / 8, static_cast<int>(std::ceil(s.ksteps / (0.5 * L)))));
+    if (s.ksteps > 1.25 * L) s.splits = std::max(1, std::min(s.ksteps / 8, static_cast<int>(std::ceil(s.ksteps / L))));
     s.kper = (s.ksteps + s.splits - 1) / s.splits;
     s.splits = (s.ksteps + s.kper - 1) / s.kper;
     s.units = s.mn * s.splits;
     pl.part_bytes[i] = s.splits > 1 ? place(static_cast<size_t>(s.splits) * s.M * s.N * 4) : 0;
   }
-  pl.pp.first = pl.pp.s[1].kper >= pl.pp.s[0].kper ? 1 : 0;
+  sdattn::ProductParams& pp = pl.pp;
+  pp.first = pp.s[1].kper >= pp.s[0].kper ? 1 : 0;
+  pp.wide = pp.s[0].bn > 256 ? 1 : 0;           // both results have C columns
+  pl.pairs = std::min(pairs, pp.s[0].units + pp.s[1].units);
+  pp.heavy = pp.s[pp.first].units % pl.pairs;
+  const int light = pl.pairs - pp.heavy, n2 = pp.s[1 - pp.first].units;
+  pp.fill = pp.heavy == 0 ? 0 : std::min(pp.s[pp.first].kper / pp.s[1 - pp.first].kper, (n2 + light - 1) / light);
   pl.total = at;
   return pl;
 }
@@ -349,14 +357,13 @@ sdattn_status launch_ff_bwd(const sdattn_ff_desc* d, const FFBwdPlan& pl, const 
     const uint64_t M = sd.M;
     const bool ok = sd.splits > 1
                         ? make_map_3d(&mo[i], parts[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, C, M, sd.splits, C * 4, M * C * 4, 32, 32)
-                        : make_map_3d(&mo[i], outs[i], dt, C, M, 1, C * 2, M * C * 2, 64, 32);
+                        : make_map_3d(&mo[i], outs[i], dt, C, M, 1, C * 2, M * C * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return SDATTN_ERR_CUDA;
   }
   auto kern = sdattn::product_kernel<BF16>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, sdattn::ProductCfg::SMEM, done, dev)) return SDATTN_ERR_CUDA;
-  const int grid = std::min(nsm / 2, pl.pp.s[0].units + pl.pp.s[1].units) * 2;
-  if (!launch_cluster(kern, grid, 2, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
+  if (!launch_cluster(kern, pl.pairs * 2, 2, sdattn::ProductCfg::NTHREADS, sdattn::ProductCfg::SMEM, s, mpk, mpm, mw, mx, mo[0], mo[1], pl.pp))
     return SDATTN_ERR_CUDA;
   sdattn::FinishParams f = {};
   int64_t work = 0;

@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 
 // ---------------------------------------------------------------------------
 // dx = P W and dW = P^T x in one launch, on CTA pairs.  A unit is a 256-row
-// tile of one of the two results, up to 256 of its columns, over one split of
-// the contraction; units of both results are dealt out in turn, so that
+// tile of one of the two results, up to 320 of its columns, over one split of
+// the contraction; units of both results are dealt out together, so that
 // neither product leaves SMs idle while the other runs.
 //   dx: A = P [T][2F], K-major;  B = W [2F][C], N-major (its rows run along N)
 //   dW: A = P, M-major (P^T);    B = x [T][C], N-major
@@ -560,21 +560,22 @@ struct ProductCfg {
   static constexpr int BK = 64;
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int SLAB = 64 * 128;             // 64 columns x 64 contraction rows
-  static constexpr int BN = 256;                    // most columns of a tile, half of them in each CTA
-  static constexpr int STAGE = A_BYTES + BN / 2 / 64 * SLAB;
-  static constexpr int STAGES = 6;
-  static constexpr int OFF_STG = STAGES * STAGE;    // [8 warps] 32 rows x 128 bytes
-  static constexpr int OFF_BAR = OFF_STG + 8 * 4096;
+  static constexpr int BN = 320;                    // most columns of a tile, half of them in each CTA
+  static constexpr int STAGE = A_BYTES + 3 * SLAB;
+  static constexpr int STAGES = 4;
+  static constexpr int EPI = 16;                    // epilogue warps
+  static constexpr int OFF_STG = STAGES * STAGE;    // [EPI] 32 rows x 32 columns of up to 4 bytes
+  static constexpr int OFF_BAR = OFF_STG + EPI * 4096;
   static constexpr int NBAR = 2 * STAGES + 4 + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-  static constexpr int NTHREADS = 384;
+  static constexpr int NTHREADS = (4 + EPI) * 32;
   static constexpr uint32_t TMEM_COLS = 512;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct ProductSide {
   int M, N;           // the result's rows and columns
-  int bn;             // columns per tile, a multiple of 64 up to 256
+  int bn;             // columns per tile, a multiple of 64 up to 320
   int nts;            // column tiles
   int mn;             // row tiles (of 256) x column tiles
   int splits;         // of the contraction
@@ -584,8 +585,28 @@ struct ProductSide {
 
 struct ProductParams {
   ProductSide s[2];   // 0: dx, 1: dW
-  int first;          // the side whose units are longer: dealt out before the other's
+  int first;          // the side whose units are longer
+  int wide;           // tiles of more than 256 columns: one accumulator
+  // The long units go to the pairs in turn; the pairs [heavy, pairs) then have
+  // one fewer and get up to `fill` short units each, at most a long one's worth
+  // and no more than their even share; the others go to all pairs in turn.
+  int heavy, fill;
 };
+
+// The k-th unit of a pair, or -1.
+__device__ __forceinline__ int product_deal(const ProductParams& p, int pair, int pairs, int k) {
+  const int n1 = p.s[p.first].units, n2 = p.s[1 - p.first].units;
+  const int longs = (n1 - pair + pairs - 1) / pairs;
+  if (k < longs) return pair + k * pairs;
+  k -= longs;
+  if (pair >= p.heavy) {
+    const int own = min(max(n2 - (pair - p.heavy) * p.fill, 0), p.fill);
+    if (k < own) return n1 + (pair - p.heavy) * p.fill + k;
+    k -= own;
+  }
+  const int u = min(n2, (pairs - p.heavy) * p.fill) + pair + k * pairs;
+  return u < n2 ? n1 + u : -1;
+}
 
 struct ProductUnit {
   int side, m0, n0, cols, half, split, k0, k1;
@@ -602,7 +623,7 @@ __device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, int 
   r.m0 = mt * 256;
   r.n0 = nt * s.bn;
   r.cols = min(s.bn, s.N - r.n0);
-  r.half = (r.cols + 31) / 32 * 16;                 // columns of B in each CTA
+  r.half = r.cols > 256 ? 160 : (r.cols + 31) / 32 * 16;   // columns of B in each CTA
   r.k0 = r.split * s.kper;
   r.k1 = min(s.ksteps, r.k0 + s.kper);
   return r;
@@ -627,7 +648,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
   volatile uint32_t* abort_flag = misc + 1;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int units = p.s[0].units + p.s[1].units, u0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -636,7 +657,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 16);
+      mbar_init(&acc_empty[i], 2 * C::EPI);
     }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
@@ -667,7 +688,9 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     RingWalk ring(bempty, C::STAGES, 1);
     uint32_t c = 0;
     bool live = true;
-    for (int u = u0; u < units && live; u += ustep) {
+    for (int ui = 0; live; ++ui) {
+      const int u = product_deal(p, pair, pairs, ui);
+      if (u < 0) break;
       const ProductUnit t = product_unit(p, u);
       const int slabs = (t.half + 63) / 64, m = t.m0 + rank * 128, n = t.n0 + rank * t.half;
       for (int ks = t.k0; ks < t.k1; ++ks, ++c) {
@@ -681,11 +704,13 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
           load_elect_pair(s, &tmPk, k, m, 0, bar);
           load_elect_pair(s + C::A_BYTES, &tmW, n, k, 0, bar);
           if (slabs > 1) load_elect_pair(s + C::A_BYTES + C::SLAB, &tmW, n + 64, k, 0, bar);
+          if (slabs > 2) load_elect_pair(s + C::A_BYTES + 2 * C::SLAB, &tmW, n + 128, k, 0, bar);
         } else {
           load_elect_pair(s, &tmPm, m, k, 0, bar);
           load_elect_pair(s + C::SLAB, &tmPm, m + 64, k, 0, bar);
           load_elect_pair(s + C::A_BYTES, &tmX, n, k, 0, bar);
           if (slabs > 1) load_elect_pair(s + C::A_BYTES + C::SLAB, &tmX, n + 64, k, 0, bar);
+          if (slabs > 2) load_elect_pair(s + C::A_BYTES + 2 * C::SLAB, &tmX, n + 128, k, 0, bar);
         }
       }
     }
@@ -699,12 +724,14 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
     RingWalk ring(bfull, C::STAGES, 0);
-    uint32_t ui = 0;
     bool live = true;
-    for (int u = u0; u < units && live; u += ustep, ++ui) {
+    for (uint32_t ui = 0; live; ++ui) {
+      const int u = product_deal(p, pair, pairs, ui);
+      if (u < 0) break;
       const ProductUnit t = product_unit(p, u);
-      const uint32_t ab = ui & 1, na = ui >> 1;
-      const uint32_t idesc = idesc_f16(256, 2 * t.half, BF16, t.side == 1, true);
+      const uint32_t ab = p.wide ? 0 : ui & 1, na = p.wide ? ui : ui >> 1;
+      const uint32_t idesc = idesc_f16(256, 2 * min(t.half, 128), BF16, t.side == 1, true);
+      const uint32_t idesc2 = idesc_f16(256, 64, BF16, t.side == 1, true);   // each CTA's columns from 128 on
       // A: 32 bytes along a K-major row, or 16 contraction rows of an M-major slab, per 16 of K
       const uint64_t adesc = sdesc_sw128(sbase, t.side == 1 ? C::SLAB : 16, 1024), astep = t.side == 1 ? 128 : 2;
       const uint64_t bdesc = sdesc_sw128(sbase + C::A_BYTES, C::SLAB, 1024);
@@ -719,6 +746,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
         tc_fence_after();
         const uint64_t off = st * (C::STAGE >> 4);
         mma_ss4_pair(tmem + ab * 256, adesc + off, bdesc + off, idesc, acc, astep, 128);
+        if (t.half > 128) mma_ss4_pair(tmem + 256, adesc + off, bdesc + off + 2 * (C::SLAB >> 4), idesc2, acc, astep, 128);
         mma_commit_pair(bempty + 8 * st);
         acc = 1;
       }
@@ -729,43 +757,50 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
     wait_warp(smem_u32(drain_bar), 0, kSiteAccFull, &never);
   } else if (warp >= 4) {
     // ------------------------------ epilogue ----------------------------------
-    const int quarter = warp & 3, half = (warp - 4) >> 2, ew = warp - 4;
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stg = smem + C::OFF_STG + ew * 4096;
-    uint32_t ui = 0;
-    for (int u = u0; u < units; u += ustep, ++ui) {
+    uint8_t* stg = smem + C::OFF_STG + (warp - 4) * 4096;
+    for (uint32_t ui = 0;; ++ui) {
+      const int u = product_deal(p, pair, pairs, ui);
+      if (u < 0) break;
       const ProductUnit t = product_unit(p, u);
       const ProductSide& sd = p.s[t.side];
       const CUtensorMap* tmO = t.side == 0 ? &tmO0 : &tmO1;
-      const uint32_t ab = ui & 1, na = ui >> 1;
+      const uint32_t ab = p.wide ? 0 : ui & 1, na = p.wide ? ui : ui >> 1;
       const int r0 = t.m0 + rank * 128 + quarter * 32;
       if (!wait_warp(bacc_full + 8 * ab, na & 1, kSiteAccFull, abort_flag)) break;
       tc_fence_after();
       const bool f32 = sd.splits > 1;
-      const int cw = f32 ? 32 : 64;             // columns per staged piece of 128 bytes
-      // the two warps of a quarter take the pieces in turn; pieces never cross
-      // the tile's edge (bn is a multiple of 64), TMA clips at the result's
+      auto release = [&]() {                    // as in gated_kernel
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
+      };
+      // pieces of 32 columns, the four warps of a quarter in turn; TMA clips at
+      // the result's edges
+      if (part * 32 >= t.cols || r0 >= sd.M) release();
 #pragma unroll 1
-      for (int c0 = half * cw; c0 < t.cols && r0 < sd.M; c0 += 2 * cw) {
+      for (int c0 = part * 32; c0 < t.cols && r0 < sd.M; c0 += 128) {
+        // where a wide tile's column lies: each CTA's first 128, then the others
+        const int q = c0 >= t.half ? 1 : 0, l = c0 - q * t.half;
+        const int at = t.half <= 128 ? c0 : l < 128 ? q * 128 + l : 256 + q * 32 + l - 128;
+        uint32_t v[32];
+        tmem_ld_x32(tmem + ab * 256 + at + lane_off, v);
+        tmem_wait_ld();
+        reg_fence<32>(v);
+        if (c0 + 128 >= t.cols) release();
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-#pragma unroll 1
-        for (int cc = 0; cc < cw; cc += 32) {
-          uint32_t v[32];
-          tmem_ld_x32(tmem + ab * 256 + c0 + cc + lane_off, v);
-          tmem_wait_ld();
-          reg_fence<32>(v);
-          if (f32) {
+        if (f32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          } else {
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(stg + lane * 128 + (((cc / 8 + q) ^ (lane & 7)) << 4)) =
-                  pack8<BF16>(reinterpret_cast<const float*>(v) + 8 * q);
-          }
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
+                pack8<BF16>(reinterpret_cast<const float*>(v) + 8 * j);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -774,9 +809,6 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
           bulk_commit();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(cluster_addr(bacc_empty + 8 * ab, 0));
     }
     if (lane == 0) bulk_wait<0>();
   }

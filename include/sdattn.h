@@ -35,6 +35,12 @@
  * filtering with 4x4 tiles:
  *      -> sdattn_wino_filter, sdattn_wino_conv3x3
  *
+ * The rest of the transformer block around attention (not in the paper): layer
+ * norm, the gated feed-forward with its projections, both with their backward
+ * passes, and the projections, with low-rank adapters for each request:
+ *      -> sdattn_layer_norm, sdattn_layer_norm_bwd, sdattn_gated_ff,
+ *         sdattn_gated_ff_bwd, sdattn_adapter_linear
+ *
  * The page gives no formula for L and S.  This library reads them as
  *      L_i = max_j A_ij,     S_i = sum_j exp(A_ij - L_i)      (natural base)
  * with A = scale * Q K^T, so that softmax(A)_ij = exp(A_ij - L_i) / S_i.

@@ -184,3 +184,34 @@ def test_refusals():
 def test_no_device_error_after_adapters():
     status, detail = sd.device_error()
     assert status == "SDATTN_OK", (status, hex(detail))
+
+
+def test_few_rows_without_an_adapter_among_them():
+    """The per-row form (fewer than 16 rows a request) where some or all requests have none."""
+    x, w, b, down, up, scale, _ = make(29, 70, 3, 128, 200, 40, 6, torch.float16)
+    for ids in (torch.full((70,), -1), torch.arange(70) % 8 - 1):
+        ids = ids.to(torch.int32).to(DEV)
+        y = sd.adapter_linear(x, w, b, down, up, scale, ids)
+        check(y, x, w, b, down, up, scale, ids, torch.float16)
+
+
+def test_many_adapters_in_a_tile_of_long_requests():
+    """Requests of 16 rows, eight adapters a tile, ranks that fill a phase
+    each: tiles of an even and an odd number of phases, one after the other."""
+    for R, L in ((64, 8), (64, 3), (16, 8), (200, 5)):
+        x, w, b, down, up, scale, _ = make(31 + R + L, 600, 16, 64, 200, R, L, torch.bfloat16)
+        ids = (torch.randint(-1, L, (600,), generator=torch.Generator().manual_seed(R)).to(torch.int32)).to(DEV)
+        y = sd.adapter_linear(x, w, b, down, up, scale, ids)
+        check(y, x, w, b, down, up, scale, ids, torch.bfloat16)
+
+
+def test_two_streams_at_once():
+    a = make(37, 48, 1, 320, 640, 32, 12, torch.float16)
+    want = sd.adapter_linear(*a)
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([sd.adapter_linear(*a) for _ in range(3)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for ys in got for y in ys)

@@ -238,3 +238,17 @@ def test_refusals():
 def test_no_device_error_after_gated_ff():
     status, detail = sd.device_error()
     assert status == "SDATTN_OK", (status, hex(detail))
+
+
+def test_gates_of_every_size():
+    """One row per gate, h = 1: infinities, not-a-numbers, far tails and zeros."""
+    vals = [float("inf"), float("nan"), 100.0, 30.0, 8.0, 5.6, 3.0, 1.0, 1e-20, 0.0, -1e-20, -1.0, -3.0, -5.6, -8.0, -30.0]
+    x = torch.eye(16, dtype=torch.float16, device=DEV)
+    w = torch.zeros(32, 16, dtype=torch.float16, device=DEV)
+    b = torch.cat([torch.ones(16), torch.tensor(vals)]).to(DEV)
+    y = sd.gated_ff(x, w, b)[0].double()
+    assert torch.isinf(y[0]) and torch.isnan(y[1])
+    g = torch.tensor(vals[2:], dtype=torch.float64, device=DEV)
+    ref = g * 0.5 * torch.erfc(-g / 2 ** 0.5)
+    u = HALF_STEP[torch.float16]
+    assert bool(((y[2:] - ref).abs() <= u * ref.abs() + 1.2e-7 + SUB[torch.float16]).all())

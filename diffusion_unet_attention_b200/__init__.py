@@ -526,10 +526,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     desc, C, need = _ln_plan((x.shape, x.dtype, at), 0.0, _meta(dy), _meta(stats), True)
     g = _vector(gamma, C, at, "gamma")
     dy, x, stats = _contig(dy), _contig(x), _contig(stats)
-    dx, dg, db = torch.empty_like(x), x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
-    ws = x.new_empty(need, dtype=torch.uint8)
+    dx = torch.empty_like(x)
+    dg = x.new_empty(C, dtype=torch.float32) if g is None else torch.empty_like(g)
+    db = torch.empty_like(dg)
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _call(at, "sdattn_layer_norm_bwd", desc, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(g),
-          dx.data_ptr(), dg.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
+          dx.data_ptr(), dg.data_ptr(), db.data_ptr(), _ptr(ws), need)
     return dx, dg, db
 
 
@@ -579,7 +581,7 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     b = _vector(bias, 2 * F, at, "bias")
     dy, x, w = _contig(dy), _contig(x), _contig(w)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
-    db = x.new_empty(2 * F, dtype=torch.float32) if bias is not None else None
+    db = torch.empty_like(b) if b is not None else None
     ws = x.new_empty(need, dtype=torch.uint8)
     _call(at, "sdattn_gated_ff_bwd", desc, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(b),
           dx.data_ptr(), dw.data_ptr(), _ptr(db), ws.data_ptr(), need)

@@ -405,10 +405,20 @@ sdattn_status check_adapter(const sdattn_adapter_desc* d) {
   return SDATTN_OK;
 }
 
-// Whether the adapters are per-row work: requests of fewer than 16 rows, and D
+// Ranks per slot of a phase, and slots per adapter (adapter.cuh).
+int adapter_rc(const sdattn_adapter_desc* d) { return std::max(16, std::min(64, (d->R + 15) / 16 * 16)); }
+int adapter_chunks(const sdattn_adapter_desc* d) { return std::max(1, (d->R + 63) / 64); }
+
+// Whether the adapters are per-row work: requests of fewer than 16 rows whose
+// adapters could fill three phases or more of a tile (two more passes over x
+// cost less than the second launch, its workspace and the reads per row), and D
 // and U read anew for every row are at most 64 MB (about 8 us out of L2).
 bool adapter_rows(const sdattn_adapter_desc* d) {
-  return d->L > 0 && d->rows < 16 && d->T * d->R * (static_cast<int64_t>(d->C) + d->K) * 2 <= (int64_t(64) << 20);
+  if (d->L == 0 || d->rows >= 16) return false;
+  const int64_t distinct = std::min<int64_t>(std::min<int64_t>(d->T / d->rows, (128 + d->rows - 1) / d->rows + 1), d->L);
+  const int spp = sdattn::AdapterCfg::ZN / adapter_rc(d);
+  return distinct * adapter_chunks(d) > 2 * spp &&
+         d->T * d->R * (static_cast<int64_t>(d->C) + d->K) * 2 <= (int64_t(64) << 20);
 }
 
 size_t adapter_ws_bytes(const sdattn_adapter_desc* d) {
@@ -461,8 +471,8 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.L = d->L;
   p.R = d->R;
   p.rows = d->rows;
-  p.rc = std::max(16, std::min(64, (d->R + 15) / 16 * 16));
-  p.chunks = std::max(1, (d->R + 63) / 64);
+  p.rc = adapter_rc(d);
+  p.chunks = adapter_chunks(d);
   p.tm = static_cast<int>(std::min<uint64_t>(128, (T + 7) / 8 * 8));
   p.bn = plan_adapter(d, p.tm, MMA ? p.rc : 0, ROWS ? Cfg::BN_ROWS : Cfg::BN, nsm);
   p.rts = static_cast<int>((T + p.tm - 1) / p.tm);

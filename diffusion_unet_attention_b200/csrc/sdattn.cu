@@ -1099,7 +1099,7 @@ size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc) {
   int64_t grid = 1;
   for (bool vec : {false, true})
     if (!vec || ln_vec(desc, {})) grid = std::max(grid, ln_bwd_grid(desc, plan_ln(desc, vec, true, nsm), nsm));
-  return static_cast<size_t>(grid) * 2 * desc->C * sizeof(float);
+  return grid <= 1 ? 0 : static_cast<size_t>(grid) * 2 * desc->C * sizeof(float);   // one CTA writes the sums themselves
 }
 
 sdattn_status sdattn_layer_norm(const sdattn_ln_desc* desc, const void* X, const float* gamma, const float* beta,
@@ -1139,7 +1139,7 @@ sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, 
   const int nsm = sm_count(dev);
   const LNPlan pl = plan_ln(desc, ln_vec(desc, {dY, X, dX, gamma}), true, nsm);
   const int64_t grid = ln_bwd_grid(desc, pl, nsm);   // 0 without rows: the sums are zero
-  if (!ws || ws_bytes < static_cast<size_t>(grid) * 2 * desc->C * sizeof(float)) return SDATTN_ERR_WORKSPACE;
+  if (grid > 1 && (!ws || ws_bytes < static_cast<size_t>(grid) * 2 * desc->C * sizeof(float))) return SDATTN_ERR_WORKSPACE;
   if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   sdattn::LNParams p = {};

@@ -341,7 +341,8 @@ typedef struct {
 sdattn_status sdattn_layer_norm(const sdattn_ln_desc* desc, const void* X, const float* gamma, const float* beta,
                                 void* Y, float* stats, void* stream);
 
-/* Bytes of workspace sdattn_layer_norm_bwd needs on the current device; 0 for an invalid desc. */
+/* Bytes of workspace sdattn_layer_norm_bwd needs on the current device; 0 when
+ * it needs none (few rows), and for an invalid desc. */
 size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc);
 
 /* Layer normalisation, backward pass, from the forward's inputs and stats
@@ -351,7 +352,7 @@ size_t sdattn_layer_norm_bwd_workspace_bytes(const sdattn_ln_desc* desc);
  * dY, X, stats, gamma (or NULL: ones): inputs; dX, dgamma, dbeta (float32
  * [C]): outputs, all written (zero sums when T = 0).  The sums run in a fixed
  * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-
- * owned, overwritten, no state between calls.  At most two launches. */
+ * owned, overwritten, no state between calls; NULL / 0 when none is needed.  At most two launches. */
 sdattn_status sdattn_layer_norm_bwd(const sdattn_ln_desc* desc, const void* dY, const void* X, const float* stats,
                                     const float* gamma, void* dX, float* dgamma, float* dbeta, void* ws,
                                     size_t ws_bytes, void* stream);
@@ -421,13 +422,13 @@ size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc);
  * float32 [K] or NULL; ids: int32 [T / rows] in device memory, or NULL for the
  * plain projection (then D, U and scale must be NULL too); scale: float32 [L]
  * or NULL (ones).  Requests may name adapters in any order and share them.
- * Requests of many rows run in one launch, in which scale[i] X D[i]^T is
- * rounded to dtype once, as the second product's operand, and each distinct
- * adapter among a tile's 128 rows costs one more small product; requests of
- * fewer than 16 rows, while D and U read once per row stay below 64 MB, run
+ * Mostly one launch, in which scale[i] X D[i]^T is rounded to dtype once, as
+ * the second product's operand, and the distinct adapters among a tile's 128
+ * rows cost it more small products.  Requests of fewer than 16 rows that may
+ * name so many adapters that this would mean three or more passes over X run
  * in two launches through ws (16-byte aligned, caller-owned, overwritten, no
- * state between calls; else NULL / 0 will do), without that rounding.  T = 0
- * does nothing. */
+ * state between calls; else NULL / 0 will do), without that rounding, as long
+ * as D and U read once per row stay below 64 MB.  T = 0 does nothing. */
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
                                     const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
                                     void* ws, size_t ws_bytes, void* stream);

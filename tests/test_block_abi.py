@@ -43,6 +43,7 @@ def test_layer_norm_pointers(lib):
     assert fwd(ln(), OK, ODD, OK, OK, OK, None) == 3
     assert fwd(ln(), OK, OK, OK, OK, OFF4, None) == 3
     assert fwd(ln(T=0), None, None, None, None, None, None) == 0     # nothing to do
+    assert lib.sdattn_layer_norm_bwd_workspace_bytes(ln(T=3)) == 0
     need = lib.sdattn_layer_norm_bwd_workspace_bytes(ln())
     assert need >= 2 * 320 * 4
     assert bwd(ln(), OK, OK, OK, None, OK, OK, OK, None, need, None) in (4, 5)      # 5: no device to plan for
@@ -121,7 +122,8 @@ def test_adapter_pointers(lib):
     assert f(ad(), OK, OK, OK, OK, OK, OK, ctypes.c_void_p((1 << 20) + 2), OK) == 3
     assert f(ad(T=0), *[None] * 8) == 0
     # requests of a few rows need a workspace: z [T][R] in fp32
-    few = dict(T=48, rows=1, R=32)
+    few = dict(T=48, rows=1, R=32, L=12)
+    assert lib.sdattn_adapter_linear_workspace_bytes(ad(T=48, rows=1, R=32)) == 0   # two adapters at most
     assert lib.sdattn_adapter_linear_workspace_bytes(ad(**few)) == 48 * 32 * 4
     assert lib.sdattn_adapter_linear_workspace_bytes(ad()) == 0
     assert f(ad(**few), *[OK] * 8) == 4

@@ -11,10 +11,10 @@
 // A tile is 128 rows by bn columns.  The D rows of the tile's adapters lie
 // behind W's in shared memory, so one product of bn + 16 .. 64 columns gives
 // x W^T and z = x D^T side by side, with no second pass over x; z goes
-// from tensor memory through registers (scaled by s in fp32, zeroed in the
-// rows of other adapters, rounded to 16 bits: the next product's operand) back
-// to tensor memory, and as the A operand of z U^T adds onto the same fp32
-// accumulator as x W^T.  Nothing but x, W, the adapters in use and y touches
+// from tensor memory through registers (scaled by s in fp32, rounded to 16
+// bits: the next product's operand) back to tensor memory, and as the A operand
+// of z U^T adds onto the same fp32 accumulator as x W^T, in the lanes of that
+// adapter's rows alone: a request never meets another's U, infinities included.  Nothing but x, W, the adapters in use and y touches
 // global memory, and W and x are never copied per request.
 //
 // Rows of different adapters may share a tile.  The planner warp lists a
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
               const uint32_t bar = bfull + 8 * st;
               expect_tx_elect(bar, p.bn * 128);
               load_elect(sbase + st * p.stage + off_w, &tmU, sl % p.chunks * 64, pend_n0, pl->adapter[sl / p.chunks], bar);
-                ++c;
+              ++c;
             }
             if (!live) break;
             if (pend_last) arrive_elect(smem_u32(&plan_empty[pend_pb]));
@@ -433,18 +433,21 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             tc_fence_after();
             const int nu = slots_of(pend_slots, pend_ph);
             for (int j = 0; j < nu; ++j) {
-              uint32_t st;
+              uint32_t st, others[4];           // rows of other adapters
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                others[q] = __ballot_sync(0xffffffffu, plans[pend_pb].place[lane + 32 * q] != (pend_ph * spp + j) / p.chunks);
               live = ring.take(st, kSiteVFull, abort_flag);
               if (!live) break;
               tc_fence_after();
               const uint64_t ud = wdesc + st * (p.stage >> 4);
               for (int kk = 0; kk < p.rc / 16; ++kk) {
                 const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column
-                mma_ts(tmem + pend_ab * C::TM_TILE, tmem + pend_zr * C::TM_TILE + p.bn + r / 32 * 32 + r % 32 / 2,
-                       ud + 2 * kk, idesc_w, 1u);
+                mma_ts_lanes(tmem + pend_ab * C::TM_TILE, tmem + pend_zr * C::TM_TILE + p.bn + r / 32 * 32 + r % 32 / 2,
+                             ud + 2 * kk, idesc_w, others);
               }
               mma_commit_at(bempty + 8 * st);
-              }
+            }
             if (!live) break;
             if (pend_last) {
               mma_commit_at(smem_u32(&acc_full[pend_ab]));
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       live = wait_warp(smem_u32(&plan_full[pb]), (ui / C::PLANS) & 1, kSiteTicket, abort_flag);
       if (!live) break;
       const AdapterPlan* pl = &plans[pb];
-      const int count = pl->count, slots = pl->slots, tile_phases = pl->phases, place = pl->place[r];
+      const int count = pl->count, slots = pl->slots, tile_phases = pl->phases;
       const float scale = pl->scale[r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&plan_empty[pb]);
@@ -513,14 +516,15 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
           tmem_wait_ld();
           reg_fence<32>(v);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {         // 16 ranks belong to one slot
-            const int slot = ph * spp + (j0 + g * 16) / p.rc;
-            const bool mine = slot / p.chunks == place;
+          for (int g = 0; g < 4; ++g) {
+            // ranks past R: zeros also where x is not finite
+            const int at = j0 + 8 * g, slot = ph * spp + at / p.rc;
+            const bool rank = slot % p.chunks * 64 + at % p.rc < p.R;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float a = mine ? __uint_as_float(v[16 * g + 2 * j]) * scale : 0.f;
-              const float b = mine ? __uint_as_float(v[16 * g + 2 * j + 1]) * scale : 0.f;
-              w[8 * g + j] = pack2<BF16>(a, b);
+            for (int j = 0; j < 4; ++j) {
+              const float a = rank ? __uint_as_float(v[8 * g + 2 * j]) * scale : 0.f;
+              const float b = rank ? __uint_as_float(v[8 * g + 2 * j + 1]) * scale : 0.f;
+              w[4 * g + j] = pack2<BF16>(a, b);
             }
           }
           tmem_st_x16(zt, w);                   // over its own columns of z

@@ -111,6 +111,18 @@ __device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
+// D[tmem] += A[tmem] B[smem]^T over 16 of K in the lanes whose bit of `off` is
+// clear; the other lanes of D keep their values, whatever their products are.
+__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // CTA pairs (cta_group::2): the two CTAs of a cluster, on neighbouring SMs,
 // run one tcgen05.mma of twice the rows.  Each holds its own 128 rows of A and

@@ -215,3 +215,27 @@ def test_two_streams_at_once():
             got.append([sd.adapter_linear(*a) for _ in range(3)])
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for ys in got for y in ys)
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+@pytest.mark.parametrize("R", [8, 16, 72])
+def test_up_matrices_that_are_not_finite_stay_with_their_requests(R, dtype):
+    """Several requests a tile, one of whose U holds infinities and NaN."""
+    x, w, b, down, up, scale, _ = make(41 + R, 12, 30, 64, 136, R, 4, dtype)
+    ids = torch.tensor([0, 1, 2, 3, -1, 0, 1, 2, 3, -1, 2, 1], dtype=torch.int32, device=DEV)
+    clean = sd.adapter_linear(x, w, b, down, up, scale, ids)
+    up2 = up.clone()
+    up2[2, :, 1], up2[2, 5, 3] = float("inf"), float("nan")
+    y = sd.adapter_linear(x, w, b, down, up2, scale, ids)
+    assert torch.equal(y[ids != 2], clean[ids != 2])
+    assert not torch.isfinite(y[ids == 2]).any() and torch.isnan(y[ids == 2][..., 5]).all()
+
+
+def test_an_infinite_product_is_infinite_whatever_the_padding():
+    """Rank 8 fills half a slot: its other half must not turn an infinity into NaN."""
+    x, w, _, down, up, _, _ = make(43, 4, 40, 64, 72, 8, 2, torch.float16)
+    x, w, down, up = x.abs() + 1, w.abs() + 0.5, down.abs() + 0.5, up.abs() + 0.5
+    x[1, 7, 3] = float("inf")
+    ids = torch.tensor([0, 1, 0, -1], dtype=torch.int32, device=DEV)
+    y = sd.adapter_linear(x, w, None, down, up, None, ids)
+    assert torch.isinf(y[1, 7]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[1, :7]).all()

@@ -461,12 +461,17 @@ def _meta(t: torch.Tensor | None):
     return None if t is None else (t.shape, t.dtype, t.get_device())
 
 
-def _out(out: torch.Tensor | None, x: torch.Tensor, shape) -> torch.Tensor:
-    """The output: `out` if it fits, else a new tensor of x's dtype."""
+def _out(out: torch.Tensor | None, x: torch.Tensor, shape, *others: torch.Tensor | None) -> torch.Tensor:
+    """The output: `out` if it fits and overlaps neither x nor the `others` (all contiguous), else a
+    new tensor of x's dtype."""
     if out is None:
         return x.new_empty(shape)
     if out.shape != shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {x.dtype} {list(shape)} on {x.device}")
+    first, last = out.data_ptr(), out.data_ptr() + out.nbytes
+    for t in (x, *others):
+        if t is not None and t.data_ptr() < last and first < t.data_ptr() + t.nbytes:
+            raise ValueError("out must not overlap an input")
     return out
 
 
@@ -512,7 +517,7 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     desc, C, _ = _ln_plan((x.shape, x.dtype, at), float(eps))
     g, b = _vector(gamma, C, at, "gamma"), _vector(beta, C, at, "beta")
     x = _contig(x)
-    y = torch.empty_like(x) if out is None else _out(out, x, x.shape)
+    y = torch.empty_like(x) if out is None else _out(out, x, x.shape, g, b)
     stats = x.new_empty(x.shape[:-1] + (2,), dtype=torch.float32) if return_stats else None
     _call(at, "sdattn_layer_norm", desc, x.data_ptr(), _ptr(g), _ptr(b), y.data_ptr(), _ptr(stats))
     return (y, stats) if return_stats else y
@@ -566,7 +571,7 @@ def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     desc, F, yshape, _ = _ff_plan((x.shape, x.dtype, at), _meta(w))
     b = _vector(bias, 2 * F, at, "bias")
     x, w = _contig(x), _contig(w)
-    y = _out(out, x, yshape)
+    y = _out(out, x, yshape, w, b)
     _call(at, "sdattn_gated_ff", desc, x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr())
     return y
 
@@ -648,13 +653,14 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
                                              _meta(ids))
     b = _vector(bias, K, at, "bias")
     x, w = _contig(x), _contig(w)
-    y = _out(out, x, yshape)
+    if L:
+        scale = _vector(scale, L, at, "scale")
+        ids, down, up = _contig(ids), _contig(down), _contig(up)
+    y = _out(out, x, yshape, w, b, down, up, scale, ids)
     if not L:
         _call(at, "sdattn_adapter_linear", desc, x.data_ptr(), w.data_ptr(), _ptr(b), None, None, None, None,
               y.data_ptr(), None, 0)
         return y
-    scale = _vector(scale, L, at, "scale")
-    ids, down, up = _contig(ids), _contig(down), _contig(up)
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _call(at, "sdattn_adapter_linear", desc, x.data_ptr(), w.data_ptr(), _ptr(b), down.data_ptr(),
           up.data_ptr(), _ptr(scale), ids.data_ptr(), y.data_ptr(), _ptr(ws), need)

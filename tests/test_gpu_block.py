@@ -146,3 +146,18 @@ def test_feed_forward_half_trains(T, C, dtype):
 def test_no_device_error_after_block():
     status, detail = sd.device_error()
     assert status == "SDATTN_OK", (status, hex(detail))
+
+
+def test_an_output_over_an_input_is_refused():
+    x = torch.randn(40, 64, dtype=torch.float16, device=DEV)
+    both = torch.zeros(200, 64, dtype=torch.float16, device=DEV)
+    w = both[:64]
+    with pytest.raises(ValueError, match="overlap"):
+        sd.layer_norm(x, out=x)
+    with pytest.raises(ValueError, match="overlap"):
+        sd.adapter_linear(x, w, out=x)
+    with pytest.raises(ValueError, match="overlap"):
+        sd.adapter_linear(x, w, out=both[63:103])
+    with pytest.raises(ValueError, match="overlap"):
+        sd.gated_ff(x, torch.cat([w, w]), out=x)
+    assert sd.adapter_linear(x, w, out=both[64:104]).eq(0).all()

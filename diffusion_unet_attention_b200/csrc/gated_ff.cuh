@@ -34,6 +34,13 @@
 
 namespace sdattn {
 
+// Measured (C = 320, F = 1280): forward of 8192 rows 15 us (900 TFLOP/s), of
+// 65536 rows 92-97 us (1.1-1.2 PFLOP/s, 70% of a library product's best rate);
+// the products alone take 70 us of the latter, the epilogue's arithmetic alone
+// 73 us (about 2000 clocks each a tile), which overlap but for the hand-offs.
+// Backward of 8192 rows 57 us (cold, under a profiler, 34 us here and 29 us in
+// product_kernel).
+
 // GELU of a pair of gates on packed fp32 pairs (half the instructions of two
 // scalars).  With q = erfc(|g| / sqrt 2) / 2, the normal tail,
 //   Phi(g) = 1 - q for g >= 0 and q below,  so  GELU(g) = max(g, 0) - |g| q.
@@ -587,6 +594,11 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 // B.  M- and N-major tiles are slabs of 64 columns x 64 contraction rows,
 // 128-byte swizzled.  A result whose contraction is split goes to fp32
 // partials that finish_kernel adds in split order.
+//
+// Bound by operand loads: a step of a 320-column tile brings 40 KB to each SM,
+// some 900 clocks at the 45 bytes per clock that L2 gives every SM at once,
+// against 640 clocks of products.  (8192 rows, C = 320, F = 1280: both products,
+// 26.8 GFLOP, in 29 us cold; a warp each for A's and B's loads changed nothing.)
 // ---------------------------------------------------------------------------
 struct ProductCfg {
   static constexpr int BK = 64;

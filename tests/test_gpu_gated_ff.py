@@ -252,3 +252,14 @@ def test_gates_of_every_size():
     ref = g * 0.5 * torch.erfc(-g / 2 ** 0.5)
     u = HALF_STEP[torch.float16]
     assert bool(((y[2:] - ref).abs() <= u * ref.abs() + 1.2e-7 + SUB[torch.float16]).all())
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+@pytest.mark.parametrize("T,C,F", [(500, 1280, 5048), (8300, 320, 1240)])
+def test_more_tiles_than_pairs(T, C, F, dtype):
+    """A few tiles of CTA pairs behind the last full wave, the last column tile narrow."""
+    x, w, b, dy = make(T + 7 * C + F, T, C, F, dtype)
+    check_forward(x, w, b, sd.gated_ff(x, w, b), dtype)
+    got = sd.gated_ff_backward(dy, x, w, b)
+    check_backward(x, w, b, dy, got, dtype)
+    assert all(torch.equal(p, q) for p, q in zip(got, sd.gated_ff_backward(dy, x, w, b)))

@@ -396,12 +396,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
       }
       if (!more) break;
     }
-    // every load lands before the CTA can exit
-    volatile uint32_t never = 0;
-    for (uint32_t st = 0; st < NS && st < c; ++st) {
-      const uint32_t uses = (c - st + NS - 1) / NS;
-      wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
-    }
+    drain_ring(bfull, NS, c, kSiteKFull);
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc_w = idesc_f16(128, p.bn, BF16, false, false);

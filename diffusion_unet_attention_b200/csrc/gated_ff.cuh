@@ -331,14 +331,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
         }
       }
     }
-    // every load lands before the CTA (or its pair) can exit
-    if (rank == 0) {
-      volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < static_cast<uint32_t>(nstages) && st < c; ++st) {
-        const uint32_t uses = (c - st + nstages - 1) / nstages;
-        wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
-      }
-    }
+    drain_ring(rank == 0 ? bfull : bempty, nstages, c, rank == 0 ? kSiteKFull : kSiteKEmpty);
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
     const uint32_t idesc = idesc_f16(TROWS, 2 * hn, BF16, false, false);
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();        // neither CTA leaves while the other's products read its memory
+  if constexpr (PAIR) pair_exit(smem_u32(drain_bar), rank);
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) {
@@ -758,13 +751,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
         }
       }
     }
-    if (rank == 0) {
-      volatile uint32_t never = 0;
-      for (uint32_t st = 0; st < C::STAGES && st < c; ++st) {
-        const uint32_t uses = (c - st + C::STAGES - 1) / C::STAGES;
-        wait_warp(bfull + 8 * st, (uses - 1) & 1, kSiteKFull, &never);
-      }
-    }
+    drain_ring(rank == 0 ? bfull : bempty, C::STAGES, c, rank == 0 ? kSiteKFull : kSiteKEmpty);
   } else if (warp == 1 && rank == 0) {
     // ------------------------------ MMA issuer --------------------------------
     RingWalk ring(bfull, C::STAGES, 0);
@@ -859,7 +846,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                            // neither CTA leaves while the other's products read its memory
+  pair_exit(smem_u32(drain_bar), rank);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM_COLS);

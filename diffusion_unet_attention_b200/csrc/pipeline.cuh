@@ -63,6 +63,19 @@ struct RingWalk {
   }
 };
 
+// Waits for the last phase of every stage that c turns of a ring used, so that
+// what still arrives in this CTA's shared memory lands before the CTA exits: a
+// CTA's own loads; in a pair, the leader waits for both CTAs' loads and the
+// other CTA for the leader's commits that empty its stages.  An abort elsewhere
+// does not cut it short; its own limit is one second in all.
+__device__ __forceinline__ void drain_ring(uint32_t bars, uint32_t n, uint32_t c, uint32_t site) {
+  volatile uint32_t never = 0;
+  for (uint32_t st = 0; st < n && st < c; ++st) {
+    const uint32_t uses = (c - st + n - 1) / n;
+    wait_warp(bars + 8 * st, (uses - 1) & 1, site, &never);
+  }
+}
+
 // --------------------------- issued by a converged warp ---------------------------
 __device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
   asm volatile(
@@ -196,6 +209,20 @@ __device__ __forceinline__ void mma_commit_at(uint32_t bar) {
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
+}
+
+// The end of a pair's work, by all threads of both CTAs.  The leader's last
+// commit arrives on `drain` in both CTAs, after all its products and earlier
+// commits; the leader's issuing warp has waited for its own.  The other CTA
+// waits for its copy, which would otherwise be on its way to shared memory that
+// the CTA has left.  Then neither CTA leaves while the other's products read
+// its memory.
+__device__ __forceinline__ void pair_exit(uint32_t drain, int rank) {
+  if (rank != 0 && threadIdx.x >> 5 == 1) {
+    volatile uint32_t never = 0;
+    wait_warp(drain, 0, kSiteAccFull, &never);
+  }
+  cluster_sync();
 }
 
 // An arrival on a barrier of either CTA.  (Released at cluster scope it costs

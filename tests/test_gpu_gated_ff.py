@@ -263,3 +263,25 @@ def test_more_tiles_than_pairs(T, C, F, dtype):
     got = sd.gated_ff_backward(dy, x, w, b)
     check_backward(x, w, b, dy, got, dtype)
     assert all(torch.equal(p, q) for p, q in zip(got, sd.gated_ff_backward(dy, x, w, b)))
+
+
+def test_pairs_back_to_back():
+    """Short launches of CTA pairs, one after the other and mixed with single
+    CTAs whose barriers lie elsewhere in shared memory: every CTA must have all
+    that arrives in its memory behind it when it leaves.  An arrival that came
+    late would complete a phase of a later kernel's barrier."""
+    a = make(43, 8192, 320, 1280, torch.float16)
+    b = make(44, 77, 128, 72, torch.bfloat16)
+    calls = [lambda: (sd.gated_ff(*a[:3]),), lambda: sd.gated_ff_backward(a[3], *a[:3]),
+             lambda: (sd.gated_ff(*b[:3]),), lambda: (sd.adapter_linear(a[0], a[1], a[2]),),
+             lambda: sd.gated_ff_backward(b[3], *b[:3])]
+    want = [[t.clone() for t in f()] for f in calls]
+    check_forward(*a[:3], want[0][0], torch.float16)
+    check_backward(*a, want[1], torch.float16)
+    for turn in range(100):
+        got = [f() for f in calls]
+        if turn % 20 == 19:
+            for g, w in zip(got, want):
+                assert all(torch.equal(p, q) for p, q in zip(g, w)), turn
+    status, detail = sd.device_error()
+    assert status == "SDATTN_OK", (status, hex(detail))

@@ -409,44 +409,66 @@ sdattn_status check_adapter(const sdattn_adapter_desc* d) {
 int adapter_rc(const sdattn_adapter_desc* d) { return std::max(16, std::min(64, (d->R + 15) / 16 * 16)); }
 int adapter_chunks(const sdattn_adapter_desc* d) { return std::max(1, (d->R + 63) / 64); }
 
-// Whether the adapters are per-row work: requests of fewer than 16 rows whose
-// adapters could fill three phases or more of a tile (two more passes over x
-// cost less than the second launch, its workspace and the reads per row), and D
-// and U read anew for every row are at most 64 MB (about 8 us out of L2).
-bool adapter_rows(const sdattn_adapter_desc* d) {
-  if (d->L == 0 || d->rows >= 16) return false;
-  const int64_t distinct = std::min<int64_t>(std::min<int64_t>(d->T / d->rows, (128 + d->rows - 1) / d->rows + 1), d->L);
-  const int spp = sdattn::AdapterCfg::ZN / adapter_rc(d);
-  return distinct * adapter_chunks(d) > 2 * spp &&
-         d->T * d->R * (static_cast<int64_t>(d->C) + d->K) * 2 <= (int64_t(64) << 20);
-}
-
-size_t adapter_ws_bytes(const sdattn_adapter_desc* d) {
-  return adapter_rows(d) ? static_cast<size_t>(d->T) * d->R * sizeof(float) : 0;
-}
-
 // Columns per tile (16, 48, or a multiple of 32, up to `most`, so that equal
 // pieces of whole 16-byte units go to at most four warps): the fewest waves of the
 // longest of a tile's products (2 clocks per column and 64 of C, the adapters'
 // ranks included), issue (300 clocks a step), loads (45 bytes per clock and SM)
 // and epilogue, plus one epilogue at the end.
-int plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int most, int nsm) {
+struct AdapterTiles {
+  int bn;
+  double waves, clocks;
+};
+
+AdapterTiles plan_adapter(const sdattn_adapter_desc* d, int tm, int rc, int most, int nsm) {
   const int64_t rts = (d->T + tm - 1) / tm;
   const double ksteps = (d->C + 63) / 64;
-  int best_bn = most;
-  double best = 1e300;
+  AdapterTiles best{most, 0, 1e300};
   for (int bn = most; bn >= 16; bn -= 16) {
     if (bn % 32 != 0 && bn != 16 && bn != 48) continue;
     const int64_t tiles = rts * ((d->K + bn - 1) / bn);
     const double waves = static_cast<double>((tiles + nsm - 1) / nsm);
     const double step = std::max(std::max(2.0 * (bn + rc), 300.0), 128.0 * (tm + bn + rc) / 45.0);
-    const double cost = waves * std::max(ksteps * step, 12.0 * bn) + 12.0 * bn;
-    if (cost < best) {
-      best = cost;
-      best_bn = bn;
-    }
+    const double clocks = waves * std::max(ksteps * step, 12.0 * bn) + 12.0 * bn;
+    if (clocks < best.clocks) best = {bn, waves, clocks};
   }
-  return best_bn;
+  return best;
+}
+
+int adapter_tm(const sdattn_adapter_desc* d) { return static_cast<int>(std::min<int64_t>(128, (d->T + 7) / 8 * 8)); }
+
+// Whether the adapters are per-row work: requests of fewer than 16 rows whose
+// adapters could fill three phases or more of a tile, where that is expected
+// to be the cheaper form.  Which adapters meet in a tile is on the device; the
+// one-launch form costs between one adapter a tile (best) and as many as its
+// rows allow (worst): a phase past the first another pass over x and D (380
+// clocks a step, or its loads), a slot past the first 1400 clocks, a tile's
+// hand-off 4000.  The per-row form costs a launch and D and U read for every
+// row (2000 bytes a clock).  It is taken where rows^2 < best * worst, so that
+// neither form can lose by more than the square root of worst / best.  One
+// adapter a tile, random ids, per-row form, measured: 64 rows of 1600 to 2560,
+// 32 adapters of rank 128: 18, 326, 35 us (per row); 300 rows of 1280, 200 of
+// rank 64: 12, 477, 39 (per row); 48 rows of 1280, 12 of rank 32: 10, 40, 9
+// (per row); 64 requests of 8 rows of 1280, 32 of rank 64: 15, 110, 44 (one
+// launch); 16384 rows of 320, 16 of rank 8: 16, 43, 64 (one launch).
+bool adapter_rows(const sdattn_adapter_desc* d, int nsm) {
+  if (d->L == 0 || d->T == 0 || d->rows >= 16) return false;
+  if (d->T * d->R > (int64_t(1) << 24)) return false;   // z: 64 MB of workspace at most
+  const int rc = adapter_rc(d), spp = sdattn::AdapterCfg::ZN / rc, chunks = adapter_chunks(d), tm = adapter_tm(d);
+  const int64_t distinct = std::min<int64_t>(std::min<int64_t>(d->T / d->rows, (128 + d->rows - 1) / d->rows + 1), d->L);
+  if (distinct * chunks <= 2 * spp) return false;
+  const AdapterTiles mma = plan_adapter(d, tm, rc, sdattn::AdapterCfg::BN, nsm);
+  const AdapterTiles plain = plan_adapter(d, tm, 0, sdattn::AdapterCfg::BN_ROWS, nsm);
+  const double pass = (d->C + 63) / 64 * std::max(380.0, 128.0 * (tm + sdattn::AdapterCfg::ZN) / 45.0);
+  auto launch = [&](int64_t adapters) {
+    const int64_t slots = adapters * chunks, phases = (slots + spp - 1) / spp;
+    return 4000.0 + mma.clocks + mma.waves * (4000.0 + (phases - 1) * pass + (slots - 1) * 1400.0);
+  };
+  const double rows = 8000.0 + plain.clocks + static_cast<double>(d->T) * d->R * (d->C + d->K) * 2.0 / 2000.0;
+  return rows * rows < launch(1) * launch(distinct);
+}
+
+size_t adapter_ws_bytes(const sdattn_adapter_desc* d, int nsm) {
+  return adapter_rows(d, nsm) ? static_cast<size_t>(d->T) * d->R * sizeof(float) : 0;
 }
 
 template <bool BF16, int MODE>
@@ -473,8 +495,8 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
   p.rows = d->rows;
   p.rc = adapter_rc(d);
   p.chunks = adapter_chunks(d);
-  p.tm = static_cast<int>(std::min<uint64_t>(128, (T + 7) / 8 * 8));
-  p.bn = plan_adapter(d, p.tm, MMA ? p.rc : 0, ROWS ? Cfg::BN_ROWS : Cfg::BN, nsm);
+  p.tm = adapter_tm(d);
+  p.bn = plan_adapter(d, p.tm, MMA ? p.rc : 0, ROWS ? Cfg::BN_ROWS : Cfg::BN, nsm).bn;
   p.rts = static_cast<int>((T + p.tm - 1) / p.tm);
   p.nts = (d->K + p.bn - 1) / p.bn;
   p.ksteps = (d->C + 63) / 64;
@@ -511,10 +533,10 @@ sdattn_status launch_adapter(const sdattn_adapter_desc* d, const void* X, const 
 }
 
 template <bool BF16>
-sdattn_status dispatch_adapter(const sdattn_adapter_desc* d, const void* X, const void* W, const float* bias,
+sdattn_status dispatch_adapter(const sdattn_adapter_desc* d, bool rows, const void* X, const void* W, const float* bias,
                                const void* D, const void* U, const float* scale, const int32_t* ids, void* Y, void* ws,
                                cudaStream_t s) {
   if (!ids) return launch_adapter<BF16, sdattn::kAdapterNone>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
-  if (adapter_rows(d)) return launch_adapter<BF16, sdattn::kAdapterRows>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
+  if (rows) return launch_adapter<BF16, sdattn::kAdapterRows>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
   return launch_adapter<BF16, sdattn::kAdapterMma>(d, X, W, bias, D, U, scale, ids, Y, ws, s);
 }

@@ -1203,7 +1203,8 @@ sdattn_status sdattn_gated_ff_bwd(const sdattn_ff_desc* desc, const void* dY, co
 
 size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc) {
   if (check_adapter(desc) != SDATTN_OK) return 0;
-  return adapter_ws_bytes(desc);
+  const int dev = current_device();
+  return adapter_ws_bytes(desc, sm_count(dev < 0 ? 0 : dev));
 }
 
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
@@ -1217,13 +1218,15 @@ sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void*
   if (!aligned16(X) || !aligned16(W) || !aligned16(bias) || !aligned16(D) || !aligned16(U) || !aligned16(Y) ||
       !aligned_to(scale, 4) || !aligned_to(ids, 4))
     return SDATTN_ERR_ALIGNMENT;
-  if (ids && adapter_rows(desc)) {
-    if (!ws || ws_bytes < adapter_ws_bytes(desc)) return SDATTN_ERR_WORKSPACE;
+  const int dev = current_device();
+  const bool rows = ids && adapter_rows(desc, sm_count(dev < 0 ? 0 : dev));
+  if (rows) {
+    if (!ws || ws_bytes < static_cast<size_t>(desc->T) * desc->R * sizeof(float)) return SDATTN_ERR_WORKSPACE;
     if (!aligned16(ws)) return SDATTN_ERR_ALIGNMENT;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SDATTN_BF16 ? dispatch_adapter<true>(desc, X, W, bias, D, U, scale, ids, Y, ws, s)
-                                    : dispatch_adapter<false>(desc, X, W, bias, D, U, scale, ids, Y, ws, s);
+  return desc->dtype == SDATTN_BF16 ? dispatch_adapter<true>(desc, rows, X, W, bias, D, U, scale, ids, Y, ws, s)
+                                    : dispatch_adapter<false>(desc, rows, X, W, bias, D, U, scale, ids, Y, ws, s);
 }
 
 const char* sdattn_status_string(sdattn_status status) {

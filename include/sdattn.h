@@ -410,8 +410,8 @@ typedef struct {
     int32_t dtype;    /* sdattn_dtype of X, W, D, U and Y */
 } sdattn_adapter_desc;
 
-/* Bytes of workspace sdattn_adapter_linear needs for this shape with ids; 0
- * when it needs none, and for an invalid desc. */
+/* Bytes of workspace sdattn_adapter_linear needs for this shape with ids on the
+ * current device (at most 64 MB); 0 when it needs none, and for an invalid desc. */
 size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc);
 
 /* A projection shared by many requests, each with a low-rank adapter of its
@@ -427,8 +427,8 @@ size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc);
  * rows cost it more small products.  Requests of fewer than 16 rows that may
  * name so many adapters that this would mean three or more passes over X run
  * in two launches through ws (16-byte aligned, caller-owned, overwritten, no
- * state between calls; else NULL / 0 will do), without that rounding, as long
- * as D and U read once per row stay below 64 MB.  T = 0 does nothing. */
+ * state between calls; else NULL / 0 will do), without that rounding, where
+ * reading D and U once per row is expected to cost less.  T = 0 does nothing. */
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
                                     const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,
                                     void* ws, size_t ws_bytes, void* stream);

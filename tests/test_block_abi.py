@@ -129,3 +129,15 @@ def test_adapter_pointers(lib):
     assert f(ad(**few), *[OK] * 8) == 4
     assert f(ad(**few), *[OK] * 8, ws=OK, n=48 * 32 * 4 - 1) == 4
     assert f(ad(**few), *[OK] * 8, ws=OFF4, n=48 * 32 * 4) == 3
+
+
+def test_adapter_form_follows_its_cost(lib):
+    """Single rows with an adapter each take the per-row form (it has a
+    workspace) at widths on both sides of 64 MB of adapters read, 26 us as
+    against 330; many rows of few ranks that may share adapters do not."""
+    ws = lib.sdattn_adapter_linear_workspace_bytes
+    for C, K in ((1560, 2520), (1600, 2560)):
+        assert ws(ad(T=64, rows=1, C=C, K=K, R=128, L=32)) == 64 * 128 * 4
+    assert ws(ad(T=300, rows=1, C=1280, K=1280, R=64, L=200)) == 300 * 64 * 4
+    assert ws(ad(T=16384, rows=1, R=8, L=16)) == 0
+    assert ws(ad(T=(1 << 27) - 1, rows=1, C=8, K=8, R=256, L=1 << 20)) == 0      # never more than 64 MB

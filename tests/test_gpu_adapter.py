@@ -239,3 +239,30 @@ def test_an_infinite_product_is_infinite_whatever_the_padding():
     ids = torch.tensor([0, 1, 0, -1], dtype=torch.int32, device=DEV)
     y = sd.adapter_linear(x, w, None, down, up, None, ids)
     assert torch.isinf(y[1, 7]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[1, :7]).all()
+
+
+def workspace(G, N, C, K, R, L):
+    from ctypes import byref
+    from diffusion_unet_attention_b200 import _lib
+    return sd.load_library().sdattn_adapter_linear_workspace_bytes(byref(_lib.AdapterDesc(G * N, C, K, L, R, N, 0)))
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+@pytest.mark.parametrize("G,N,C,K,R,L", [(4096, 1, 320, 320, 72, 160), (1300, 3, 72, 136, 72, 300), (256, 4, 640, 640, 128, 256),
+                                         (4000, 2, 72, 136, 200, 90), (7, 16, 320, 328, 256, 7)])
+def test_many_adapters_a_tile_in_one_launch(G, N, C, K, R, L, dtype):
+    """Short requests in the one-launch form: up to 128 adapters in a tile of
+    128 rows, each of several slots; a tile of fewer rows too (7 x 16)."""
+    assert workspace(G, N, C, K, R, L) == 0
+    x, w, b, down, up, scale, _ = make(G + R, G, N, C, K, R, L, dtype)
+    ids = ((torch.arange(G) * 37) % (L + 1) - 1).to(torch.int32).to(DEV)      # all different in a tile
+    y = sd.adapter_linear(x, w, b, down, up, scale, ids)
+    check(y, x, w, b, down, up, scale, ids, dtype)
+    assert torch.equal(y, sd.adapter_linear(x, w, b, down, up, scale, ids))
+
+
+@pytest.mark.parametrize("G,N,C,K,R,L", [(64, 1, 1600, 2560, 128, 32), (64, 1, 1560, 2520, 128, 32), (300, 1, 1280, 1280, 64, 200)])
+def test_per_row_form_of_wide_adapters(G, N, C, K, R, L):
+    assert workspace(G, N, C, K, R, L) == G * N * R * 4
+    a = make(G + R, G, N, C, K, R, L, torch.float16)
+    check(sd.adapter_linear(*a), *a, torch.float16)

@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) pair_exit(smem_u32(drain_bar), rank);
+  if constexpr (PAIR) pair_exit(smem_u32(drain_bar));
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) {
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(ProductCfg::NTHREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  pair_exit(smem_u32(drain_bar), rank);
+  pair_exit(smem_u32(drain_bar));
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM_COLS);

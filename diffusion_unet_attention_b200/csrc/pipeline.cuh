@@ -217,8 +217,8 @@ __device__ __forceinline__ void mma_commit_at(uint32_t bar) {
 // waits for its copy, which would otherwise be on its way to shared memory that
 // the CTA has left.  Then neither CTA leaves while the other's products read
 // its memory.
-__device__ __forceinline__ void pair_exit(uint32_t drain, int rank) {
-  if (rank != 0 && threadIdx.x >> 5 == 1) {
+__device__ __forceinline__ void pair_exit(uint32_t drain) {
+  if (threadIdx.x >> 5 == 1 && cluster_rank() != 0) {
     volatile uint32_t never = 0;
     wait_warp(drain, 0, kSiteAccFull, &never);
   }

@@ -62,21 +62,24 @@ __device__ __forceinline__ float nan_max0(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint64_t gelu_pair(uint64_t g) {
+// Takes half the gates, u = g / 2 (an exact scaling, folded into the bias's
+// addition): max(g, 0) = u + |u| costs what a maximum does, and at a gate of
+// -infinity it is the formula's not-a-number.
+__device__ __forceinline__ uint64_t gelu_pair(uint64_t u) {
   const auto both = [](float c) { return f2_pack(c, c); };
-  float g0, g1, e0, e1;
-  f2_unpack(g, g0, g1);
-  // the bound keeps an infinite gate from meeting q = 0
-  const uint64_t m = f2_pack(fmaxf(-fabsf(g0), -kTailBound), fmaxf(-fabsf(g1), -kTailBound));
-  uint64_t y = f2_fma(m, both(kTail7), both(kTail6));
-  y = f2_fma(m, y, both(kTail5));
-  y = f2_fma(m, y, both(kTail4));
-  y = f2_fma(m, y, both(kTail3));
-  y = f2_fma(m, y, both(kTail2));
-  y = f2_fma(m, y, both(kTail1));
-  y = f2_fma(m, y, both(kTail0));
+  float u0, u1, e0, e1;
+  f2_unpack(u, u0, u1);
+  // the bound keeps a gate of +infinity from meeting q = 0
+  const uint64_t m = f2_pack(fmaxf(-fabsf(u0), -0.5f * kTailBound), fmaxf(-fabsf(u1), -0.5f * kTailBound));
+  uint64_t y = f2_fma(m, both(128.f * kTail7), both(64.f * kTail6));
+  y = f2_fma(m, y, both(32.f * kTail5));
+  y = f2_fma(m, y, both(16.f * kTail4));
+  y = f2_fma(m, y, both(8.f * kTail3));
+  y = f2_fma(m, y, both(4.f * kTail2));
+  y = f2_fma(m, y, both(2.f * kTail1));
+  y = f2_fma(m, y, both(1.f + kTail0));      // log2 of 2 q
   f2_unpack(y, e0, e1);
-  return f2_fma(m, f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_pack(nan_max0(g0), nan_max0(g1)));
+  return f2_fma(m, f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_pack(u0 + fabsf(u0), u1 + fabsf(u1)));
 }
 
 // GELU and its slope Phi(g) + g phi(g) for a pair of gates, for the backward
@@ -96,8 +99,9 @@ __device__ __forceinline__ GeluGrad gelu_grad_pair(uint64_t g) {
   const auto both = [](float c) { return f2_pack(c, c); };
   float g0, g1, d0, d1, e0, e1, t0, t1, s0, s1;
   f2_unpack(g, g0, g1);
-  // q is 0 far below 64: the bound keeps an infinite gate from meeting it
-  const uint64_t mag = f2_pack(fminf(fabsf(g0), 64.f), fminf(fabsf(g1), 64.f));
+  // q is 0 far below 64: the bound keeps a gate of +infinity from meeting it
+  // (-infinity meets it and gives the formula's not-a-number)
+  const uint64_t mag = f2_pack(fmaxf(fminf(fabsf(g0), 64.f), -g0), fmaxf(fminf(fabsf(g1), 64.f), -g1));
   f2_unpack(f2_fma(mag, both(kP), both(1.f)), d0, d1);
   f2_unpack(f2_mul(f2_mul(g, g), both(kE)), e0, e1);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));
@@ -182,7 +186,8 @@ struct GatedParams {
 };
 
 // y (or dh and dg) of 8 columns of one row, from the accumulators and the
-// columns' biases in shared memory (the same address in every lane).
+// columns' biases in shared memory (the same address in every lane; forward, the
+// gates' are halved).
 template <bool BWD, bool BF16>
 __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t* g, const float* bh, const float* bg,
                                                const uint4& dy, float* o0, float* o1) {
@@ -196,15 +201,15 @@ __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t
       const int e = 4 * q + 2 * k;
       const uint64_t hp = f2_add(f2_pack(__uint_as_float(h[e]), __uint_as_float(h[e + 1])),
                                  k ? f2_pack(bv.z, bv.w) : f2_pack(bv.x, bv.y));
-      const uint64_t gp = f2_add(f2_pack(__uint_as_float(g[e]), __uint_as_float(g[e + 1])),
-                                 k ? f2_pack(gv.z, gv.w) : f2_pack(gv.x, gv.y));
+      const uint64_t ga = f2_pack(__uint_as_float(g[e]), __uint_as_float(g[e + 1]));
+      const uint64_t gb = k ? f2_pack(gv.z, gv.w) : f2_pack(gv.x, gv.y);
       if constexpr (BWD) {
-        const GeluGrad a = gelu_grad_pair(gp);
+        const GeluGrad a = gelu_grad_pair(f2_add(ga, gb));
         const uint64_t dp = f2_pack(d[e], d[e + 1]);
         f2_unpack(f2_mul(dp, a.gelu), o0[e], o0[e + 1]);
         f2_unpack(f2_mul(f2_mul(dp, hp), a.slope), o1[e], o1[e + 1]);
       } else {
-        f2_unpack(f2_mul(hp, gelu_pair(gp)), o0[e], o0[e + 1]);
+        f2_unpack(f2_mul(hp, gelu_pair(f2_fma(ga, f2_pack(0.5f, 0.5f), gb))), o0[e], o0[e + 1]);
       }
     }
   }
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(GatedCfg::NTHREADS, 1)
       for (int j = lane; j < hn; j += 32) {
         const bool ok = p.bias != nullptr && f + j < p.F;   // columns past F take none: their products are zero
         sbias[ab * 256 + j] = ok ? __ldg(p.bias + f + j) : 0.f;
-        sbias[ab * 256 + 128 + j] = ok ? __ldg(p.bias + p.F + f + j) : 0.f;
+        sbias[ab * 256 + 128 + j] = ok ? __ldg(p.bias + p.F + f + j) * (BWD ? 1.f : 0.5f) : 0.f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bias_full[ab]);

@@ -285,3 +285,22 @@ def test_pairs_back_to_back():
                 assert all(torch.equal(p, q) for p, q in zip(g, w)), turn
     status, detail = sd.device_error()
     assert status == "SDATTN_OK", (status, hex(detail))
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+def test_a_gate_of_minus_infinity(dtype):
+    """The formula gives not-a-number there, and so does `geglu`; gates far
+    below zero give zero, the largest finite ones themselves."""
+    x = torch.eye(16, dtype=dtype, device=DEV)
+    w = torch.zeros(32, 16, dtype=dtype, device=DEV)
+    gates = torch.full((16,), 1.0)
+    gates[:6] = torch.tensor([float("-inf"), float("inf"), 3e38, -20.0, -1e4, -3e38])
+    b = torch.cat([torch.ones(16), gates]).to(DEV)
+    y = sd.gated_ff(x, w, b)
+    assert torch.isnan(sd.geglu(b.to(dtype)[None])[0, 0])
+    assert torch.isnan(y[:, 0]).all() and (y[:, 1] == float("inf")).all()
+    assert torch.equal(y[:, 2], torch.full((16,), 3e38, device=DEV).to(dtype))
+    assert (y[:, 3:6].abs() <= 1e-13).all()
+    db = sd.gated_ff_backward(torch.full_like(x, 1 / 16), x, w, b)[2]      # sums of 16 equal rows
+    assert torch.isnan(db[0]) and torch.isnan(db[16]) and not db[3:6].any() and not db[19:22].any()
+    assert db[1] == float("inf") and torch.isfinite(db[2:16]).all() and torch.isfinite(db[18:]).all()

@@ -78,3 +78,14 @@ def geglu(x):
     if x.shape[-1] != 2 * F:
         raise ValueError("the last dimension must be even")
     return x[..., :F] * gelu(x[..., F:])
+
+
+def geglu_backward(dy, x, w, bias=None):
+    """Gradients (dx, dw, dbias) of sum(dy * geglu(x w^T + bias)) in fp64, x [T, C], w [2F, C], dy [T, F]."""
+    dy, x, w = (np.asarray(a, np.float64) for a in (dy, x, w))
+    p = x @ w.T + (0.0 if bias is None else np.asarray(bias, np.float64))
+    F = w.shape[0] // 2
+    h, g = p[:, :F], p[:, F:]
+    slope = 0.5 * (1.0 + erf(g / np.sqrt(2.0))) + g * np.exp(-0.5 * g * g) / np.sqrt(2.0 * np.pi)
+    dp = np.concatenate([dy * gelu(g), dy * h * slope], axis=1)
+    return dp @ w, dp.T @ x, dp.sum(axis=0)

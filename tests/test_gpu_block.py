@@ -161,3 +161,23 @@ def test_an_output_over_an_input_is_refused():
     with pytest.raises(ValueError, match="overlap"):
         sd.gated_ff(x, torch.cat([w, w]), out=x)
     assert sd.adapter_linear(x, w, out=both[64:104]).eq(0).all()
+
+
+@pytest.mark.parametrize("oracle_fn", ["layer_norm", "geglu", "geglu_backward", "layer_norm_backward"])
+def test_smoke_checks_every_output(oracle_fn, monkeypatch):
+    """An oracle whose output is off by 1% must fail smoke()."""
+    import __graft_entry__ as entry
+    from oracle import unet_ops
+    right = getattr(unet_ops, oracle_fn)
+
+    def wrong(*a):
+        r = right(*a)
+        if oracle_fn == "geglu":
+            return 1.01 * r
+        k = 0 if oracle_fn == "layer_norm" else 1            # y; dw; dgamma
+        return tuple(1.01 * t if i == k else t for i, t in enumerate(r))
+
+    entry.smoke()
+    monkeypatch.setattr(unet_ops, oracle_fn, wrong)
+    with pytest.raises(AssertionError, match="rel_frob"):
+        entry.smoke()

@@ -35,3 +35,20 @@ def test_layer_norm_gradients_are_torchs(ln_case):
     np.testing.assert_allclose(ref, y.detach().numpy(), rtol=1e-12, atol=1e-12)
     for got, want in zip(unet_ops.layer_norm_backward(dy, x, stats, gamma), (tx.grad, tg.grad, tb.grad)):
         np.testing.assert_allclose(got, want.numpy(), rtol=1e-11, atol=1e-12)
+
+
+def test_geglu_backward_against_differences():
+    rng = np.random.default_rng(11)
+    x, w, b, dy = rng.normal(size=(5, 6)), rng.normal(size=(8, 6)), rng.normal(size=8), rng.normal(size=(5, 4))
+    got = unet_ops.geglu_backward(dy, x, w, b)
+    f = lambda v: (unet_ops.geglu(v[0] @ v[1].T + v[2]) * dy).sum()   # noqa: E731
+    at, step = [x, w, b], 1e-6
+    for k, grad in enumerate(got):
+        for i in np.ndindex(at[k].shape):
+            d = np.zeros(at[k].shape)
+            d[i] = step
+            num = (f([a + d if j == k else a for j, a in enumerate(at)])
+                   - f([a - d if j == k else a for j, a in enumerate(at)])) / (2 * step)
+            # the differences' own error: step^2 of third derivatives and 2^-52 |f| / step, both below 1e-7 here
+            assert abs(num - grad[i]) <= 1e-6 * max(1.0, abs(grad[i]))
+    assert np.array_equal(unet_ops.geglu_backward(dy, x, w)[0], unet_ops.geglu_backward(dy, x, w, np.zeros(8))[0])

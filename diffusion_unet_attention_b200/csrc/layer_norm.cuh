@@ -12,8 +12,11 @@
 // a warp (L = 8, 16 or 32; several rows per warp when rows are short) or to a
 // whole CTA when it is too long for a warp's registers, so its sums are a few
 // shuffles.  The variance is the mean of squared deviations from the mean
-// (two passes over registers, no cancellation).  All arithmetic is fp32; y and
-// dx are rounded once to the element type.
+// (two passes over registers, no cancellation).  Where the mean is above eight
+// deviations a third pass takes what its rounding left off them (a constant row
+// of 2000: 1e-4, which r = 316 would make 0.04; taken off in every row it cost
+// rows of a CTA 10%).  All arithmetic is fp32; y and dx are rounded once to the
+// element type.
 //
 // The weight's gradients: every CTA runs over rows b, b + grid, ... and keeps
 // the sums of its columns in registers (a lane owns the same columns of every
@@ -188,9 +191,30 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_k
       for (int e = 0; e < E; ++e) sq = fmaf(f[e] - mean, f[e] - mean, sq);
     }
   }
-  const float rstd = 1.f / sqrtf(ln_row_sum<CTA>(sq, p.L, red) * inv + p.eps);
+  float squares = ln_row_sum<CTA>(sq, p.L, red);
+  // The mean's rounding matters where it is large beside the deviations: their
+  // own mean is what it left.  (All rows of a warp together; a CTA has one row.)
+  const bool far = live && squares * inv * 64.f < mean * mean;
+  float shift = 0.f;
+  if (__builtin_expect(CTA ? far : __any_sync(0xffffffffu, far), 0)) {
+    float dev = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (lane + u * p.L < p.nch) {
+        float f[E];
+        El::unpack(r[u], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) dev += f[e] - mean;
+      }
+    }
+    dev = ln_row_sum<CTA>(dev, p.L, red);
+    shift = dev * inv;
+    if (!far) shift = 0.f;                    // whatever rows share its warp, a row's result is the same
+    squares = fmaxf(squares - shift * dev, 0.f);
+  }
+  const float rstd = 1.f / sqrtf(fmaf(squares, inv, p.eps)), offset = -shift * rstd;
   if (!live) return;
-  if (p.stats != nullptr && lane == 0) *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(mean, rstd);
+  if (p.stats != nullptr && lane == 0) *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(mean + shift, rstd);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = lane + u * p.L;
@@ -200,7 +224,7 @@ __global__ void __launch_bounds__(CTA ? kLNRowThreads : kLNThreads) layer_norm_k
       El::params(p.gamma, i * E, 1.f, g);
       El::params(p.beta, i * E, 0.f, b);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mean) * rstd, g[e], b[e]);
+      for (int e = 0; e < E; ++e) f[e] = fmaf(fmaf(f[e] - mean, rstd, offset), g[e], b[e]);
       El::store(p.Y, at + static_cast<int64_t>(i) * E, f);
     }
   }

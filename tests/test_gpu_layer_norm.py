@@ -213,3 +213,29 @@ def test_refusals():
         sd.layer_norm_backward(x, x, st[:3])
     with pytest.raises(ValueError):
         sd.layer_norm_backward(x, x, st.cpu())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [77, 1000, 1001, 4095])
+def test_constant_rows_of_large_values(dtype, C):
+    """z is 0 where no value of a row differs, whatever the mean's rounding."""
+    v = torch.tensor([1999.0, 1234.5, 777.7, -1601.3, 3.1], dtype=dtype, device=DEV)
+    y, stats = sd.layer_norm(v[:, None].repeat(1, C), return_stats=True)
+    # the deviations are a few steps of the value, their mean right to 2^-20 of them, and r at most 317
+    assert bool((y.double().abs() <= 317 * 2.0 ** -20 * 64 * E32 * v.double().abs()[:, None]).all())
+    assert bool(((stats[:, 0].double() - v.double()).abs() <= 2 * E32 * v.double().abs()).all())
+
+
+@pytest.mark.parametrize("C", [320, 1000, 1001, 4095])
+def test_small_deviations_from_a_large_mean(C):
+    """fp32 rows around 1000 with deviations of 0.01.  x - m is exact (both
+    within a factor of two), so what errs is the deviations' mean, their squares
+    and the product: 64 steps of |d| + mean |d|, not of |x|."""
+    x = (1000 + 0.01 * torch.randn(40, C, generator=torch.Generator().manual_seed(C), dtype=torch.float64)).float()
+    xs = x.double().numpy()
+    ref = unet_ops.layer_norm(xs, np.ones(C), np.zeros(C), 1e-6)[0]
+    d = np.abs(xs - xs.mean(-1, keepdims=True))
+    r = 1 / np.sqrt((d ** 2).mean(-1, keepdims=True) + 1e-6)
+    y = sd.layer_norm(x.to(DEV), eps=1e-6).double().cpu().numpy()
+    bnd = E32 * np.abs(ref) + 64 * E32 * (r * (d + d.mean(-1, keepdims=True)) + np.abs(ref))
+    assert np.all(np.abs(y - ref) <= bnd), np.max(np.abs(y - ref) / bnd)

@@ -11,11 +11,12 @@
 // A tile is 128 rows by bn columns.  The D rows of the tile's adapters lie
 // behind W's in shared memory, so one product of bn + 16 .. 64 columns gives
 // x W^T and z = x D^T side by side, with no second pass over x; z goes
-// from tensor memory through registers (scaled by s in fp32, rounded to 16
-// bits: the next product's operand) back to tensor memory, and as the A operand
+// from tensor memory through registers (scaled by s in fp32, then as two 16-bit
+// parts, the next product's operands) back to tensor memory, and as the A operand
 // of z U^T adds onto the same fp32 accumulator as x W^T, in the lanes of that
-// adapter's rows alone: a request never meets another's U, infinities included.  Nothing but x, W, the adapters in use and y touches
-// global memory, and W and x are never copied per request.
+// adapter's rows alone: a request never meets another's U, infinities included.
+// Nothing but x, W, the adapters in use and y touches global memory, and W and x
+// are never copied per request.
 //
 // Rows of different adapters may share a tile.  The planner warp lists a
 // tile's distinct adapters; each contributes ceil(R / 64) slots of rc ranks
@@ -133,6 +134,21 @@ __global__ void __launch_bounds__(256) adapter_z_kernel(const uint16_t* __restri
     const float s = scale != nullptr ? __ldg(scale + id) : 1.f;
     *reinterpret_cast<float2*>(z + static_cast<int64_t>(t) * R + r) = make_float2(a * s, b * s);
   }
+}
+
+// a as the sum of two values of the element type, right to 2^-13 (bf16) or 2^-19
+// (fp16) of a: rounded once, z would add as much again to y's error as y's own
+// rounding, and a request's y would depend on which form its call takes.  hi is
+// a little below a in magnitude, so that lo is never zero beside it and has its
+// sign: both parts' products with an infinite U are the formula's infinity.
+template <bool BF16>
+__device__ __forceinline__ void split_z(float a, float& hi, float& lo) {
+  if constexpr (BF16) {
+    hi = __uint_as_float(__float_as_uint(a * (1.f - 0x1p-7f)) & 0xffff0000u);
+  } else {
+    hi = __half2float(__float2half_rz(a * (1.f - 0x1p-10f)));
+  }
+  lo = fabsf(a) < __int_as_float(0x7f800000) ? a - hi : a;   // an infinity twice
 }
 
 // One tile's plan in shared memory.
@@ -463,9 +479,10 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
               tc_fence_after();
               const uint64_t ud = wdesc + st * (p.stage >> 4);
               for (int kk = 0; kk < p.rc / 16; ++kk) {
-                const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column
-                mma_ts_lanes(tmem + pend_ab * C::TM_TILE, tmem + pend_zr * C::TM_TILE + p.bn + r / 32 * 32 + r % 32 / 2,
-                             ud + 2 * kk, idesc_w, others);
+                const int r = j * p.rc + kk * 16;   // rank within the phase: two per tensor-memory column, 32 ranks' parts together
+                const uint32_t z = tmem + pend_zr * C::TM_TILE + p.bn + r / 32 * 32 + r % 32 / 2;
+                mma_ts_lanes(tmem + pend_ab * C::TM_TILE, z, ud + 2 * kk, idesc_w, others);
+                mma_ts_lanes(tmem + pend_ab * C::TM_TILE, z + 16, ud + 2 * kk, idesc_w, others);
               }
               mma_commit_at(bempty + 8 * st);
             }
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
 #pragma unroll 1
         for (int j0 = 0; j0 < ranks; j0 += 32) {
           const uint32_t zt = tmem + ((ui + ph) & 1) * C::TM_TILE + p.bn + j0 + lane_off;
-          uint32_t v[32], w[16];
+          uint32_t v[32], w[16], x[16];
           tmem_ld_x32(zt, v);
           tmem_wait_ld();
           reg_fence<32>(v);
@@ -543,12 +560,15 @@ __global__ void __launch_bounds__(AdapterCfg::NTHREADS, 1)
             const bool rank = slot % p.chunks * 64 + at % p.rc < p.R;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float a = rank ? __uint_as_float(v[8 * g + 2 * j]) * scale : 0.f;
-              const float b = rank ? __uint_as_float(v[8 * g + 2 * j + 1]) * scale : 0.f;
-              w[4 * g + j] = pack2<BF16>(a, b);
+              float ah, al, bh, bl;
+              split_z<BF16>(rank ? __uint_as_float(v[8 * g + 2 * j]) * scale : 0.f, ah, al);
+              split_z<BF16>(rank ? __uint_as_float(v[8 * g + 2 * j + 1]) * scale : 0.f, bh, bl);
+              w[4 * g + j] = pack2<BF16>(ah, bh);
+              x[4 * g + j] = pack2<BF16>(al, bl);
             }
           }
-          tmem_st_x16(zt, w);                   // over its own columns of z
+          tmem_st_x16(zt, w);                   // over z's own columns: the upper parts, then the lower
+          tmem_st_x16(zt + 16, x);
         }
         tmem_wait_st();
         tc_fence_before();

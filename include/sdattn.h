@@ -422,12 +422,12 @@ size_t sdattn_adapter_linear_workspace_bytes(const sdattn_adapter_desc* desc);
  * float32 [K] or NULL; ids: int32 [T / rows] in device memory, or NULL for the
  * plain projection (then D, U and scale must be NULL too); scale: float32 [L]
  * or NULL (ones).  Requests may name adapters in any order and share them.
- * Mostly one launch, in which scale[i] X D[i]^T is rounded to dtype once, as
- * the second product's operand, and the distinct adapters among a tile's 128
+ * Mostly one launch, in which scale[i] X D[i]^T is held as the sum of two values
+ * of dtype, the second product's operands, and the distinct adapters among a tile's 128
  * rows cost it more small products.  Requests of fewer than 16 rows that may
  * name so many adapters that this would mean three or more passes over X run
  * in two launches through ws (16-byte aligned, caller-owned, overwritten, no
- * state between calls; else NULL / 0 will do), without that rounding, where
+ * state between calls; else NULL / 0 will do), where
  * reading D and U once per row is expected to cost less.  T = 0 does nothing. */
 sdattn_status sdattn_adapter_linear(const sdattn_adapter_desc* desc, const void* X, const void* W, const float* bias,
                                     const void* D, const void* U, const float* scale, const int32_t* ids, void* Y,

@@ -266,3 +266,41 @@ def test_per_row_form_of_wide_adapters(G, N, C, K, R, L):
     assert workspace(G, N, C, K, R, L) == G * N * R * 4
     a = make(G + R, G, N, C, K, R, L, torch.float16)
     check(sd.adapter_linear(*a), *a, torch.float16)
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+@pytest.mark.parametrize("G,N,C,K,R,L", [(2, 77, 768, 320, 8, 2), (16, 64, 320, 320, 16, 8), (9, 40, 128, 136, 40, 4),
+                                         (5, 64, 320, 328, 72, 3), (3, 300, 64, 200, 256, 2)])
+def test_the_low_rank_product_is_held_in_two_parts(G, N, C, K, R, L, dtype):
+    """Where the shared projection is zero y is z U^T alone, and sums that
+    cancel show z's own rounding: 2^-13 (bf16) or 2^-19 (fp16, and half a
+    subnormal step) of |z| |U|^T beside the fp32 sums' and y's own half step."""
+    x, w, _, down, up, scale, ids = make(53 + R, G, N, C, K, R, L, dtype)
+    ids = (torch.arange(G, device=DEV, dtype=torch.int32)) % L
+    up[:, :, R // 2:] = -up[:, :, :R // 2]                  # pairs of ranks whose products nearly cancel
+    down[:, R // 2:] = down[:, :R // 2]
+    down[:, 0] *= 1.5
+    y = sd.adapter_linear(x, torch.zeros_like(w), None, down, up, scale, ids).double()
+    part = {torch.float16: 2.0 ** -19, torch.bfloat16: 2.0 ** -13}[dtype]
+    for g, i in enumerate(ids.tolist()):
+        X, D, U, s = x[g].double(), down[i].double(), up[i].double(), float(scale[i])
+        z = s * (X @ D.T)
+        ez = s * (C + 64) * E32 * (X.abs() @ D.abs().T) + part * z.abs() + SUB[dtype]
+        ref = z @ U.T
+        bnd = ez @ U.abs().T + (2 * R + 64) * E32 * (z.abs() @ U.abs().T) + HALF_STEP[dtype] * ref.abs() + SUB[dtype]
+        assert bool(((y[g] - ref).abs() <= bnd).all()), f"off by {float(((y[g] - ref).abs() / bnd).max()):.2f} of its bound"
+
+
+@pytest.mark.parametrize("dtype", list(HALF_STEP))
+def test_an_infinite_up_matrix_gives_infinity(dtype):
+    """z of few bits (exact in one part) and of many, times one infinity."""
+    x, w, _, down, up, _, _ = make(59, 2, 40, 64, 72, 16, 1, dtype)
+    x[0] = 0
+    x[0, :, 0], down[0] = 2.0, down[0].abs() + 0.25
+    down[0, :, 0] = 0.5                                     # request 0: z = 1 in every rank
+    x[1] = x[1].abs() + 0.5
+    up[0, 3, 5], up[0, 7, 2] = float("inf"), float("-inf")
+    y = sd.adapter_linear(x, w, None, down, up, None, torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert (y[..., 3] == float("inf")).all() and (y[..., 7] == float("-inf")).all()
+    rest = [k for k in range(72) if k not in (3, 7)]
+    assert torch.isfinite(y[..., rest]).all()

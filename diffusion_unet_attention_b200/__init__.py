@@ -21,6 +21,11 @@ backward pass `layer_norm_backward`, and the gated feed-forward `gated_ff`
 and `adapter_linear`, a projection shared by requests with a low-rank adapter
 each.
 
+Autograd records none of these calls: outputs carry no graph, whatever the
+inputs require.  A training step calls the backward passes itself (the layer
+norm and the gated feed-forward have one; attention, convolution and the
+projections do not).
+
 This module only marshals torch tensors (device memory and streams) into the
 C ABI of libsdattn.so; all arithmetic runs in the CUDA kernels.  There is no
 CPU fallback: calls fail if the library or a CUDA device is missing.
@@ -509,7 +514,11 @@ def _ln_plan(xm, eps: float, dym=None, statsm=None, backward: bool = False):
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
                eps: float = 1e-5, out: torch.Tensor | None = None, return_stats: bool = False):
     """Layer normalisation over the last dimension of x [..., C] (fp16, bf16 or
-    fp32; C up to 8192), with fp32 gamma and beta [C] (None: ones, zeros).
+    fp32; C up to 8192), with fp32 gamma and beta [C] (None: ones, zeros; other
+    types are converted, a launch each, on every call).
+
+    x may start on any element; rows of whole 16-byte units on a 16-byte
+    boundary run two to four times as fast as others.
 
     With `return_stats` returns (y, stats), stats [..., 2] fp32 = (mean,
     1 / sqrt(var + eps)) of every row, as `layer_norm_backward` takes it."""
@@ -566,7 +575,8 @@ def gated_ff(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     p[..., :F] * GELU(p[..., F:]) (the activation of `geglu`), p never stored.
 
     x [..., C] and w [2F, C] (fp16 or bf16), fp32 bias [2F] or None; returns
-    [..., F].  C and F must be multiples of 8."""
+    [..., F].  C and F must be multiples of 8, and x, w and out start on a
+    16-byte boundary (a view that does not is refused: pass its clone)."""
     at = x.get_device()
     desc, F, yshape, _ = _ff_plan((x.shape, x.dtype, at), _meta(w))
     b = _vector(bias, 2 * F, at, "bias")
@@ -580,7 +590,12 @@ def gated_ff_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: 
     """Gradients of `gated_ff`: (dx, dw, dbias) from dy [..., F] and the
     forward's inputs (the projection is computed again).  dx and dw have x's
     dtype; dbias is fp32 [2F], or None without a bias.  Repeated calls give
-    identical bits."""
+    identical bits.  dy, x and w start on a 16-byte boundary.
+
+    The projection's own gradient, dy times at most |h| or |g|, is held in x's
+    dtype between the products, as it is where each layer has its own backward
+    pass: in fp16 it becomes infinite past 65504 and loses digits below 6e-5, so
+    scale the loss accordingly (dbias is summed in fp32 before that)."""
     at = x.get_device()
     desc, F, _, need = _ff_plan((x.shape, x.dtype, at), _meta(w), _meta(dy), True)
     b = _vector(bias, 2 * F, at, "bias")
@@ -645,7 +660,8 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None =
     x [G, ..., C] and w [K, C] (fp16 or bf16), fp32 bias [K] or None; down
     [L, R, C] and up [L, K, R] of x's dtype, fp32 scale [L] (None: ones), ids
     [G] int32 on x's device; without ids the plain projection.  C, K and R must
-    be multiples of 8 (pad smaller ranks with zeros once), R at most 256.
+    be multiples of 8 (pad smaller ranks with zeros once), R at most 256, and
+    x, w, down, up and out start on a 16-byte boundary.
     For requests of different lengths pass their rows as x [T, C] with one id a
     row.  Returns [G, ..., K]."""
     at = x.get_device()

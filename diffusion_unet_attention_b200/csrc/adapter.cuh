@@ -34,9 +34,10 @@
 // run (a thread per row and two columns) and leave it in shared memory.
 //
 // Measured: 16 images at 64x64 (65536 rows, C = K = 320, 8 adapters of rank 16)
-// 33 us, 2.5 TB/s, the plain projection 19.5 us (a library product: 16 us);
-// 154 rows of 768 to 320, 2 adapters, 7.3 us; 48 single rows of 1280, 12
-// adapters of rank 32, 9.3 us.  Few rows are chains of latencies.  Many rows are
+// 31.5 us, 2.7 TB/s, the plain projection 19.5 us (a library product: 18.4 us;
+// 16384 x 1280 to 1280: 52 us and 40 us); 154 rows of 768 to 320, 2 adapters,
+// 6.6 us; 48 single rows of 1280, 12 adapters of rank 32, 9.0 us.  Few rows are
+// chains of latencies.  Many rows are
 // bound by the operands' way to each SM, x and W's tile anew for every tile
 // (36 KB a step, 45 bytes per clock at best); D's third box adds 6 us to the
 // first figure whatever its size, and U and the hand-off of z 7 us.

@@ -34,12 +34,14 @@
 
 namespace sdattn {
 
-// Measured (C = 320, F = 1280): forward of 8192 rows 15 us (900 TFLOP/s), of
-// 65536 rows 92-97 us (1.1-1.2 PFLOP/s, 70% of a library product's best rate);
-// the products alone take 70 us of the latter, the epilogue's arithmetic alone
-// 73 us (about 2000 clocks each a tile), which overlap but for the hand-offs.
-// Backward of 8192 rows 57 us (cold, under a profiler, 34 us here and 29 us in
-// product_kernel).
+// Measured (C = 320, F = 1280): forward of 8192 rows 14.5 us, of 65536 rows 81 us
+// alone (1.3 PFLOP/s, 82% of a library product's best rate) and 113 us in a row,
+// where the power cap holds the clock at 1250 MHz.  With the epilogue left out
+// the latter took 70 us: the operands' way to the SMs, 32 KB a step at 43 bytes
+// a clock (the MMAs are 512 clocks of a step's 730).  With the products left out
+// it took 73 us, some 4000 clocks a tile: latency, with no pipe above a third of
+// its rate and 43% of issue slots used.  Backward of 8192 rows 57 us (cold, under
+// a profiler, 35 us here and 29 us in product_kernel).
 
 // GELU of a pair of gates on packed fp32 pairs (half the instructions of two
 // scalars).  With q = erfc(|g| / sqrt 2) / 2, the normal tail,
@@ -48,8 +50,8 @@ namespace sdattn {
 // gelu_tail_fit.py for the least largest error of q and |g| q (1e-7 in fp32
 // arithmetic) and still falling at -8, where q is 2^-48.  That is one exponential and
 // seven FMAs; gelu_erf's form takes an exponential, a reciprocal and as many
-// FMAs, and two MUFU operations a column set the epilogue's pace (16 images at
-// 64x64 100 us, this way 95 us).
+// FMAs, and two MUFU operations a column were slower (16 images at 64x64 100 us,
+// this way 95 us).
 constexpr float kTailBound = 8.f;
 constexpr float kTail0 = -0.9999998211860657f, kTail1 = 1.1511149406433105f, kTail2 = -0.4591203033924103f,
                 kTail3 = 0.05278468504548073f, kTail4 = 0.0075082783587276936f, kTail5 = 0.000494707899633795f,
@@ -219,9 +221,9 @@ __device__ __forceinline__ void gated_columns8(const uint32_t* h, const uint32_t
 // 128 or, in a pair, 256 x 2 hn x 16; two accumulators so that a tile's
 // epilogue overlaps the next tile's products), warp 2 the tiles' biases, warps
 // 4..19 epilogue: four warps per quarter of the CTA's 128 rows, dividing the
-// tile's columns.  (The epilogue sets the pace: eight warps took 123 us for 16
-// images at 64x64, two groups of eight on alternate tiles lose where a CTA has
-// an odd handful of tiles.)
+// tile's columns.  (More warps hide more of the epilogue's latency: eight took
+// 123 us for 16 images at 64x64 where sixteen took 95; two groups of eight on
+// alternate tiles lose where a CTA has an odd handful of tiles.)
 // PAIR: tiles of 256 rows by 128 columns of h, a CTA of the pair holding the h
 // rows of W's tile and the other the g rows; the results leave through shared
 // memory and TMA stores of 32 rows x 32 columns of y, or of dh and of dg, which

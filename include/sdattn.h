@@ -385,8 +385,9 @@ size_t sdattn_gated_ff_bwd_workspace_bytes(const sdattn_ff_desc* desc);
  * are computed again).  With GELU(g) = g Phi(g), GELU'(g) = Phi(g) + g phi(g):
  *   P = [dY GELU(g), dY h GELU'(g)]   [T][2F],
  *   dX = P W,  dW = P^T X,  dbias = column sums of P.
- * P is rounded to dtype once, as the products' operand; dbias (float32 [2F])
- * is summed before that rounding.  dY [T][F], X, W, bias (or NULL): inputs;
+ * P is rounded to dtype once, as the products' operand (F16: infinite past
+ * 65504, fewer digits below 2^-14); dbias (float32 [2F]) is summed before that
+ * rounding.  dY [T][F], X, W, bias (or NULL): inputs;
  * dX [T][C], dW [2F][C]: outputs of type dtype, rounded once; dbias: output
  * or NULL.  With T = 0 dW and dbias are zero-filled.  Every sum has a fixed
  * order: repeated calls give identical bits.  ws: 16-byte aligned, caller-

@@ -446,10 +446,10 @@ int adapter_tm(const sdattn_adapter_desc* d) { return static_cast<int>(std::min<
 // row (2000 bytes a clock).  It is taken where rows^2 < best * worst, so that
 // neither form can lose by more than the square root of worst / best.  One
 // adapter a tile, random ids, per-row form, measured: 64 rows of 1600 to 2560,
-// 32 adapters of rank 128: 18, 326, 35 us (per row); 300 rows of 1280, 200 of
-// rank 64: 12, 477, 39 (per row); 48 rows of 1280, 12 of rank 32: 10, 40, 9
-// (per row); 64 requests of 8 rows of 1280, 32 of rank 64: 15, 110, 44 (one
-// launch); 16384 rows of 320, 16 of rank 8: 16, 43, 64 (one launch).
+// 32 adapters of rank 128: 19, 340, 35 us (per row); 300 rows of 1280, 200 of
+// rank 64: 13, 499, 39 (per row); 48 rows of 1280, 12 of rank 32: 10, 41, 9
+// (per row); 64 requests of 8 rows of 1280, 32 of rank 64: 15, 111, 44 (one
+// launch); 16384 rows of 320, 16 of rank 8: 16, 45, 64 (one launch).
 bool adapter_rows(const sdattn_adapter_desc* d, int nsm) {
   if (d->L == 0 || d->T == 0 || d->rows >= 16) return false;
   if (d->T * d->R > (int64_t(1) << 24)) return false;   // z: 64 MB of workspace at most

@@ -133,8 +133,8 @@ def test_adapter_pointers(lib):
 
 def test_adapter_form_follows_its_cost(lib):
     """Single rows with an adapter each take the per-row form (it has a
-    workspace) at widths on both sides of 64 MB of adapters read, 26 us as
-    against 330; many rows of few ranks that may share adapters do not."""
+    workspace) at widths on both sides of 64 MB of adapters read, 35 us as
+    against 340; many rows of few ranks that may share adapters do not."""
     ws = lib.sdattn_adapter_linear_workspace_bytes
     for C, K in ((1560, 2520), (1600, 2560)):
         assert ws(ad(T=64, rows=1, C=C, K=K, R=128, L=32)) == 64 * 128 * 4
